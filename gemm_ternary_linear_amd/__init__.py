@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 from pathlib import Path
+from typing import NamedTuple
 
 import torch
 
@@ -28,7 +29,8 @@ __all__ = [
     "PATHS", "BF16", "FP16", "abi_version", "shutdown", "LIB_PATH", "probe_read", "probe_copy",
     "probe_mfma", "probe_mfma_flops", "probe_lib", "PROBE_LIB_PATH", "quantize",
     "linear_batch_noalloc", "tile", "untile",
-    "tiled_bytes", "LAYOUTS",
+    "tiled_bytes", "LAYOUTS", "fp8_quantize", "fp8_linear", "route", "Routing", "linear_experts",
+    "combine",
 ]
 
 LIB_PATH = Path(__file__).resolve().parent / "libternary.so"
@@ -46,7 +48,8 @@ EXPORTS = (
     "ternary_linear_batch", "ternary_select_path", "ternary_gemv_max_m",
     "ternary_status_string", "ternary_abi_version", "ternary_shutdown", "ternary_quantize",
     "ternary_linear_batch_noalloc", "ternary_tile", "ternary_untile", "ternary_tiled_bytes",
-    "ternary_linear_tiled",
+    "ternary_linear_tiled", "ternary_fp8_quantize", "ternary_fp8_linear", "ternary_route",
+    "ternary_route_workspace", "ternary_linear_experts", "ternary_combine",
 )
 # Every symbol include/ternary_probe.h declares (measurement probes).
 PROBE_EXPORTS = ("ternary_probe_read", "ternary_probe_read_nt", "ternary_probe_copy",
@@ -94,6 +97,15 @@ def lib() -> ctypes.CDLL:
     L.ternary_linear_batch.argtypes = [p, i32, i32, p]
     L.ternary_linear_batch_noalloc.argtypes = [p, i32, i32, p]
     L.ternary_quantize.argtypes = [p, i32, i64, i64, i64, p, p, p]
+    f32 = ctypes.c_float
+    L.ternary_fp8_quantize.argtypes = [p, i32, i64, i64, i64, i32, i32, p, p, p]
+    L.ternary_fp8_linear.argtypes = [p, p, p, p, i64, i64, i64, p, i32, p]
+    L.ternary_route.argtypes = [p, i32, i64, i64, p, i32, i32, i32, i32, i32, f32, p, p, p, p, p, p, p]
+    L.ternary_route_workspace.argtypes = [i64, i64]
+    L.ternary_route_workspace.restype = i64
+    L.ternary_linear_experts.argtypes = [p, p, i64, p, p, i64, i64, i64, i64, p, p, i64, i32, i32, p,
+                                         i32, p]
+    L.ternary_combine.argtypes = [p, i32, i64, i64, p, p, i64, i32, p, p, p]
     L.ternary_select_path.argtypes = [i64, i64, i64, i64]
     L.ternary_status_string.argtypes = [i32]
     L.ternary_status_string.restype = ctypes.c_char_p
@@ -101,7 +113,8 @@ def lib() -> ctypes.CDLL:
                "ternary_linear_batch", "ternary_select_path", "ternary_gemv_max_m",
                "ternary_abi_version", "ternary_shutdown", "ternary_quantize",
                "ternary_linear_batch_noalloc", "ternary_linear_tiled", "ternary_tile",
-               "ternary_untile"):
+               "ternary_untile", "ternary_fp8_quantize", "ternary_fp8_linear", "ternary_route",
+               "ternary_linear_experts", "ternary_combine"):
         getattr(L, nm).restype = i32
     _lib = L
     return L
@@ -376,6 +389,229 @@ def linear_batch(problems, noalloc: bool = False) -> list:
 def linear_batch_noalloc(problems) -> list:
     """linear_batch through ternary_linear_batch_noalloc."""
     return linear_batch(problems, noalloc=True)
+
+
+# ---------------------------------------------------------------- 8-bit layers and experts
+
+_OUT = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_FP8 = (torch.float8_e4m3fn, torch.uint8)
+BLOCKS = {"row": 0, "tile": 1}
+ACTS = {"none": 0, "swiglu": 1}
+SCORES = {"softmax": 0, "sigmoid": 1}
+ROWS = {"tokens": 0, "sorted": 1}
+FP8_BLOCK = 128
+
+
+def _same_device(first: torch.Tensor, *rest) -> int:
+    """The device index of contiguous tensors that all live on one device."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("all tensors must be device tensors")
+    for t in rest:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError("all tensors must be contiguous and on one device")
+    return dev
+
+
+def _call(name: str, dev: int, *args) -> None:
+    """Calls a library function on the current stream of device `dev`."""
+    fn = getattr(_lib or lib(), name)
+    if dev == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st:
+        raise TernaryError(st, name)
+
+
+def _choice(table: dict, value, name: str) -> int:
+    if value not in table:
+        raise ValueError(f"{name} must be one of {tuple(table)}")
+    return table[value]
+
+
+def _output(out, shape, dtype, dev):
+    """`out` checked, or a new tensor."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    if tuple(out.shape) != shape or out.dtype not in _OUT or not out.is_contiguous() \
+            or out.get_device() != dev:
+        raise ValueError(f"out must be a contiguous bfloat16, float16 or float32 tensor of shape {shape} "
+                         "on the inputs' device")
+    return out
+
+
+def fp8_quantize(x: torch.Tensor, block: str = "row", act: str = "none"):
+    """bf16/fp16/fp32 [M, K] -> (float8_e4m3fn [M, Kp], float32 scales), Kp = K rounded
+    up to a multiple of 128 (filled with zeros), by ternary_fp8_quantize: a scale
+    for 128 values of a row (``block="row"``, scales [M, Kp/128]: activations) or
+    for 128 rows x 128 values (``"tile"``, scales [ceil(M/128), Kp/128]: weights).
+    ``act="swiglu"`` takes [M, 2K] and quantises silu(x[:, :K]) * x[:, K:].
+    Rows may be strided (x.stride(1) == 1)."""
+    dt = _OUT.get(x.dtype)
+    if dt is None or x.dim() != 2:
+        raise ValueError("x must be a 2-D bfloat16, float16 or float32 tensor")
+    b, a = _choice(BLOCKS, block, "block"), _choice(ACTS, act, "act")
+    dev = _same_device(x)
+    M, width = x.shape
+    if width == 0 or (a and width % 2):
+        raise ValueError("x must have columns (an even number of them for swiglu)")
+    ld = x.stride(0) if M > 1 else width
+    if (x.stride(1) != 1 and width > 1) or ld < width:
+        raise ValueError("the rows of x must be contiguous and must not overlap")
+    K = width // 2 if a else width
+    kb = (K + 127) // 128
+    q = torch.empty((M, kb * 128), dtype=torch.float8_e4m3fn, device=x.device)
+    scale = torch.empty(((M + 127) // 128 if b else M, kb), dtype=torch.float32, device=x.device)
+    _call("ternary_fp8_quantize", dev, x.data_ptr(), dt, M, K, ld, b, a, q.data_ptr(), scale.data_ptr())
+    return q, scale
+
+
+def fp8_linear(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scale: torch.Tensor,
+               dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """y [M, N] = (xq * x_scale) @ (wq * w_scale)^T of block-scaled 8-bit matrices
+    (fp8_quantize with ``block="row"`` for x [M, K] and ``"tile"`` for w [N, K]), in
+    ``dtype`` (bfloat16, float16 or float32; that of ``out`` if given)."""
+    if xq.dtype not in _FP8 or wq.dtype not in _FP8 or xq.dim() != 2 or wq.dim() != 2:
+        raise ValueError("xq and wq must be 2-D float8_e4m3fn (or uint8) tensors")
+    (M, K), N = xq.shape, wq.shape[0]
+    if K == 0 or K % 128 or wq.shape[1] != K:
+        raise ValueError(f"xq [{M}, {K}] and wq {tuple(wq.shape)} must share K, a multiple of 128")
+    if x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32 \
+            or tuple(x_scale.shape) != (M, K // 128) or tuple(w_scale.shape) != ((N + 127) // 128, K // 128):
+        raise ValueError(f"scales must be float32 [{M}, {K // 128}] and [{(N + 127) // 128}, {K // 128}]")
+    dev = _same_device(xq, xq, x_scale, wq, w_scale)
+    if dtype not in _OUT:
+        raise ValueError("dtype must be bfloat16, float16 or float32")
+    out = _output(out, (M, N), dtype, dev)
+    _call("ternary_fp8_linear", dev, xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
+          M, N, K, out.data_ptr(), _OUT[out.dtype])
+    return out
+
+
+class Routing(NamedTuple):
+    """What route() gives, and linear_experts() and combine() take (ternary_route)."""
+    ids: torch.Tensor      # int32 [T, top_k]: a token's experts, best first; -1: none
+    weights: torch.Tensor  # float32 [T, top_k]: their weights
+    offsets: torch.Tensor  # int32 [E + 1]: expert e's places are offsets[e] .. offsets[e + 1] - 1
+    order: torch.Tensor    # int32 [T * top_k]: the slot t * top_k + j at each place; -1: none
+    slots: torch.Tensor    # int32 [T, top_k]: each slot's place; -1: none
+
+
+def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+          groups: int = 1, top_groups: int | None = None, renormalize: bool = True,
+          scale: float = 1.0) -> Routing:
+    """Each token's ``top_k`` experts by softmax or sigmoid scores of logits [T, E]
+    (bf16/fp16/fp32), their weights, and the slots sorted by expert.  ``bias``
+    (float32 [E]) is added for the choice only; with ``groups`` > 1 only experts of
+    the ``top_groups`` groups with the largest sums of their two best scores are
+    chosen.  Weights are divided by their sum (``renormalize``) and multiplied
+    by ``scale``.  An expert whose logit is -inf is never chosen; a token
+    without any (a padded row of -inf) takes no slots."""
+    dt = _OUT.get(logits.dtype)
+    if dt is None or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D bfloat16, float16 or float32 tensor")
+    sc = _choice(SCORES, score, "score")
+    T, E = logits.shape
+    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,)):
+        raise ValueError(f"bias must be a float32 tensor [{E}]")
+    dev = _same_device(logits, logits, bias)
+    if top_groups is None:
+        top_groups = groups
+    L = _lib or lib()
+    need = L.ternary_route_workspace(T, E)
+    if need < 0 or not 1 <= top_k <= 32:
+        raise TernaryError(min(need, 0) or -2, "ternary_route")
+    d = logits.device
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=d)
+    weights = torch.empty((T, top_k), dtype=torch.float32, device=d)
+    offsets = torch.empty(E + 1, dtype=torch.int32, device=d)
+    order = torch.empty(T * top_k, dtype=torch.int32, device=d)
+    slots = torch.empty((T, top_k), dtype=torch.int32, device=d)
+    ws = torch.empty(need, dtype=torch.uint8, device=d).data_ptr() if need else None
+    _call("ternary_route", dev, logits.data_ptr(), dt, T, E, bias.data_ptr() if bias is not None else None,
+          sc, groups, top_groups, top_k, 1 if renormalize else 0, scale, ids.data_ptr(),
+          weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), slots.data_ptr(), ws)
+    return Routing(ids, weights, offsets, order, slots)
+
+
+def _check_routing(r: Routing):
+    T, k = r.ids.shape
+    if not all(t.dtype == torch.int32 for t in (r.ids, r.offsets, r.order, r.slots)) \
+            or r.weights.dtype != torch.float32 or tuple(r.order.shape) != (T * k,) \
+            or r.slots.shape != r.ids.shape or r.weights.shape != r.ids.shape:
+        raise ValueError("routing must hold int32 ids and slots [T, k], offsets [E + 1], order [T * k] "
+                         "and float32 weights [T, k]")
+    return T, k
+
+
+def linear_experts(xq: torch.Tensor, x_scale: torch.Tensor, packed: torch.Tensor, scale: torch.Tensor,
+                   routing: Routing, K: int | None = None, rows: str = "tokens",
+                   dtype: torch.dtype = torch.bfloat16, out: torch.Tensor | None = None) -> torch.Tensor:
+    """y [T * top_k, N]: at each place of ``routing.order`` the row of x times its
+    expert's ternary weights.  xq [rows, Kp], x_scale [rows, Kp/128] from
+    fp8_quantize hold the tokens (``rows="tokens"``) or one row for each place
+    (``"sorted"``); ``packed`` holds the experts' tiled codes, uint8
+    [E, ...] with tiled_bytes(N, K) bytes each (stacked tile() results); ``scale``
+    is float16 [E, N], or [E, N, K/128] or [E, N, K/256] for groups.  ``K`` need only be
+    given where it is not Kp.  Rows of places that hold no slot (from
+    offsets[E] on) are not written."""
+    if xq.dtype not in _FP8 or xq.dim() != 2 or x_scale.dtype != torch.float32:
+        raise ValueError("xq must be 2-D float8_e4m3fn (or uint8) and x_scale float32")
+    T, k = _check_routing(routing)
+    R, (n, Kp) = T * k, xq.shape
+    if K is None:
+        K = Kp
+    if Kp != (K + 127) // 128 * 128 or tuple(x_scale.shape) != (n, Kp // 128):
+        raise ValueError(f"xq [{n}, {Kp}] and x_scale {tuple(x_scale.shape)} do not match K={K}")
+    by = _choice(ROWS, rows, "rows")
+    if n != (R if by else T):
+        raise ValueError(f"xq must hold {R if by else T} rows ({rows})")
+    if scale.dtype != torch.float16 or scale.dim() not in (2, 3):
+        raise ValueError("scale must be float16 [E, N] or [E, N, K / group size]")
+    E, N = scale.shape[:2]
+    g = -1
+    if scale.dim() == 3:
+        g = K // scale.shape[2] if scale.shape[2] else 0
+        if g not in (128, 256) or scale.shape[2] * g != K:
+            raise ValueError(f"scale {tuple(scale.shape)} holds no groups of 128 or 256 of K={K}")
+    if packed.dtype != torch.uint8 or packed.dim() < 1 or packed.shape[0] != E \
+            or packed.numel() != E * tiled_bytes(N, K):
+        raise ValueError(f"packed must be uint8 [{E}, ...] with {tiled_bytes(N, K)} bytes an expert")
+    if tuple(routing.offsets.shape) != (E + 1,):
+        raise ValueError(f"routing.offsets must hold {E + 1} values")
+    dev = _same_device(xq, xq, x_scale, packed, scale, routing.offsets, routing.order)
+    if dtype not in _OUT:
+        raise ValueError("dtype must be bfloat16, float16 or float32")
+    out = _output(out, (R, N), dtype, dev)
+    _call("ternary_linear_experts", dev, xq.data_ptr(), x_scale.data_ptr(), n, packed.data_ptr(),
+          scale.data_ptr(), E, N, K, g, routing.offsets.data_ptr(), routing.order.data_ptr(), R, k, by,
+          out.data_ptr(), _OUT[out.dtype])
+    return out
+
+
+def combine(y: torch.Tensor, routing: Routing, add: torch.Tensor | None = None,
+            out: torch.Tensor | None = None) -> torch.Tensor:
+    """out [T, N] = add + the sum of each token's rows of y [T * top_k, N] times
+    routing.weights, in y's dtype (bf16, fp16 or fp32; ternary_combine).  ``add`` ([T, N],
+    a shared expert's output or the residual) may be ``out`` itself."""
+    dt = _OUT.get(y.dtype)
+    if dt is None or y.dim() != 2:
+        raise ValueError("y must be a 2-D bfloat16, float16 or float32 tensor")
+    T, k = _check_routing(routing)
+    R, N = y.shape
+    if R != T * k:
+        raise ValueError(f"y must have {T * k} rows")
+    if add is not None and (add.dtype != y.dtype or tuple(add.shape) != (T, N)):
+        raise ValueError(f"add must match y's dtype and have shape [{T}, {N}]")
+    dev = _same_device(y, y, routing.slots, routing.weights, add)
+    out = _output(out, (T, N), y.dtype, dev)
+    if out.dtype != y.dtype:
+        raise ValueError("out must have y's dtype")
+    _call("ternary_combine", dev, y.data_ptr(), dt, R, N, routing.slots.data_ptr(),
+          routing.weights.data_ptr(), T, k, add.data_ptr() if add is not None else None, out.data_ptr())
+    return out
 
 
 # ---------------------------------------------------------------- probes

@@ -24,7 +24,8 @@ FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
 ]
 SOURCES = ["api.hip", "pack.hip", "gemv.hip", "gemv_f4.hip", "gemv_stream.hip", "gemv_valu.hip",
-           "gemm_few.hip", "gemm.hip", "simple.hip", "noalloc.hip", "workspace.hip", "quantize.hip"]
+           "gemm_few.hip", "gemm.hip", "simple.hip", "noalloc.hip", "workspace.hip", "quantize.hip",
+           "api_fp8.hip", "fp8_quantize.hip", "fp8_products.hip", "route.hip", "combine.hip"]
 PROBE_SOURCES = ["probe.hip"]
 
 

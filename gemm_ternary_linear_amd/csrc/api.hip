@@ -6,36 +6,19 @@
 #include <stdint.h>
 
 #include "../../include/ternary.h"
+#include "check.h"
 #include "internal.h"
 
 #include <algorithm>
 
+using ternary::aligned;
+using ternary::hip_status;
+using ternary::kMaxDim;
+using ternary::overlap;
+
 namespace {
 
 constexpr int kAbiVersion = 7;
-
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// [a, a+na) and [b, b+nb) overlap (byte ranges; empty ranges never overlap).
-bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
-{
-    if (na <= 0 || nb <= 0)
-        return false;
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + (uintptr_t)nb && b0 < a0 + (uintptr_t)na;
-}
-
-int hip_status(hipError_t e)
-{
-    if (e == hipSuccess)
-        return TERNARY_OK;
-    return e == ternary::kErrCaptureWorkspace ? TERNARY_ERR_WORKSPACE : TERNARY_ERR_HIP;
-}
-
-// Largest M, N or K accepted: kernels index channels, tokens and K with
-// 32-bit ints (element offsets are 64-bit) and grids stay far inside the
-// launch limits.
-constexpr int64_t kMaxDim = (int64_t)1 << 24;
 
 // The library's group value of a group_size (-1 -> 0), or -1 if unsupported.
 int group_of(int64_t group_size)

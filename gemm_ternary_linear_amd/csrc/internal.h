@@ -181,4 +181,56 @@ inline bool gemv_preferred(int64_t M, int64_t K, int group)
     return gemv_kernel_takes(GemvKernel::AUTO, M, K, group, true);
 }
 
+// ---------------------------------------------------------------- 8-bit layers and experts
+
+// A block of 128 values along K shares a scale (and 128 rows, for weights).
+constexpr int kFp8Block = 128;
+inline int64_t fp8_blocks(int64_t n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+// Codes and scales of x (fp8_quantize.hip); `dtype` a ternary_dtype.
+hipError_t launch_fp8_quantize(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx,
+                               bool tile, bool swiglu, uint8_t *q, float *scale,
+                               hipStream_t stream);
+
+// A product of 8-bit activations (fp8_products.hip): with 8-bit weights, or
+// with the ternary weights of experts.
+struct Fp8Product {
+    const uint8_t *x;
+    const float *x_scale;
+    const uint8_t *w;         // e4m3 [N, K], or tiled codes [E, tiled_bytes(N, K)]
+    const float *w_scale;     // 8-bit weights: [ceil(N/128), nb]
+    const uint16_t *t_scale;  // ternary weights: [E, N] or [E, N, K / group]
+    void *y;
+    int dtype;                // ternary_dtype of y
+    int M, N, nb;             // rows (experts: places), channels, blocks of 128 along K
+    // experts only
+    const int32_t *offsets, *order;  // order: NULL where x holds the places themselves
+    int E, group, ngroups, top_k, x_rows;
+};
+hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream);
+hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream);
+
+struct RouteArgs {
+    const void *logits;
+    const float *bias;
+    int32_t *ids;
+    float *weights;
+    int32_t *offsets, *order, *slots;
+    void *workspace;
+    int T, E, k, groups, top_groups, renormalize, sigmoid;
+    float scale;
+};
+int64_t route_workspace(int64_t T, int64_t E);
+hipError_t launch_route(const RouteArgs &a, int dtype, hipStream_t stream);
+
+struct CombineArgs {
+    const void *y, *add;
+    void *out;
+    const int32_t *slots;
+    const float *weights;
+    int64_t R;
+    int T, k, N;
+};
+hipError_t launch_combine(const CombineArgs &a, int dtype, hipStream_t stream);
+
 }  // namespace ternary

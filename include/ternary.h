@@ -92,8 +92,9 @@ typedef enum {
 /* Weight layout of a linear call (see "Tiled layout" above). */
 typedef enum { TERNARY_LAYOUT_ROWS = 0, TERNARY_LAYOUT_TILED = 1 } ternary_layout;
 
-/* Activation / output element type (2 bytes per element). */
-typedef enum { TERNARY_BF16 = 0, TERNARY_FP16 = 1 } ternary_dtype;
+/* Activation / output element type (2 bytes per element; TERNARY_FP32, 4 bytes,
+ * only where a function says so). */
+typedef enum { TERNARY_BF16 = 0, TERNARY_FP16 = 1, TERNARY_FP32 = 2 } ternary_dtype;
 
 /* Kernel path for ternary_linear_ex.  AUTO picks by M (see ternary_linear). */
 typedef enum {
@@ -337,6 +338,186 @@ int ternary_shutdown(void);
  */
 int ternary_linear_batch_noalloc(const ternary_problem *problems, int count, int dtype,
                                  hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * 8-bit layers and experts.  The layers of a ternary model that stay at 8 bits
+ * (ternary_fp8_linear), and mixtures of ternary experts, as one chain:
+ *
+ *   x   -> ternary_fp8_quantize -> ternary_fp8_linear (gate logits) -> ternary_route
+ *   xq  -> ternary_linear_experts (gate | up) -> ternary_fp8_quantize (SwiGLU)
+ *       -> ternary_linear_experts (down) -> ternary_combine
+ *
+ * An 8-bit value is an e4m3 code (OCP: 4 exponent bits, 3 fraction bits, largest
+ * 448, 0x7f / 0xff NaN, no infinities); a scale is an fp32 number for each block of
+ * 128 values along K, of one row (activations) or of 128 rows (weights): an
+ * 8-bit matrix [M, Kp] (Kp a multiple of 128) has scales [M, Kp/128] or
+ * [ceil(M/128), Kp/128], row-major, and stands for code * scale.
+ *
+ * The conventions above hold for these functions too; none of them uses a
+ * library-owned workspace, so any of them may be captured, replayed and run
+ * on several streams at once.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Values along K (and rows, for weights) that share one scale. */
+#define TERNARY_FP8_BLOCK 128
+
+/* Which values of ternary_fp8_quantize share a scale. */
+typedef enum {
+    TERNARY_BLOCK_ROW = 0,  /* 128 values of one row (activations)      */
+    TERNARY_BLOCK_TILE = 1  /* 128 rows x 128 values of each (weights)  */
+} ternary_block;
+
+/* What ternary_fp8_quantize computes before it quantises. */
+typedef enum {
+    TERNARY_ACT_NONE = 0,
+    TERNARY_ACT_SWIGLU = 1  /* silu(x[:, :K]) * x[:, K:2K], silu(g) = g / (1 + exp(-g)) */
+} ternary_act;
+
+/*
+ * ternary_fp8_quantize - e4m3 codes and block scales of a matrix.
+ *   x      [M, K] (TERNARY_ACT_SWIGLU: [M, 2K], the gate's K columns first), dtype
+ *          `dtype` (TERNARY_BF16, TERNARY_FP16 or TERNARY_FP32), row r at element
+ *          r * ldx; aligned to its elements' size.
+ *   M, K   0 <= M, 0 < K, both up to 2^24; M == 0 is a successful no-op.
+ *   ldx    elements between rows, at least the row's length.
+ *   block  a ternary_block; act a ternary_act (TERNARY_ACT_SWIGLU with
+ *          TERNARY_BLOCK_ROW only).
+ *   q      uint8 [M, Kp] output, Kp = K rounded up to a multiple of 128 (the
+ *          columns from K on are written as 0), 16-byte aligned.
+ *   scale  fp32 output, [M, Kp/128] (rows) or [ceil(M/128), Kp/128] (tiles).
+ * Rule: s = (largest |v| of the block) / 448 rounded to fp32, q = v / s rounded
+ * to fp32 and then to the nearest e4m3 code, ties to even; v is x, or the
+ * activation's fp32 result (not rounded in between).  A block with s == 0 gets
+ * codes 0.  A NaN is written as NaN and left out of its block's largest; a block with an infinity has
+ * scale infinity, its finite values the code 0 and its infinities NaN (so what it
+ * stands for is NaN throughout).  No output may overlap x or the other output.
+ */
+int ternary_fp8_quantize(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx, int block,
+                         int act, uint8_t *q, float *scale, hipStream_t stream);
+
+/*
+ * ternary_fp8_linear - y = x * w^T of block-scaled 8-bit matrices.
+ *   x, x_scale  e4m3 [M, K] and fp32 [M, K/128] (TERNARY_BLOCK_ROW).
+ *   w, w_scale  e4m3 [N, K] and fp32 [ceil(N/128), K/128] (TERNARY_BLOCK_TILE).
+ *   M, N, K     M >= 0, N >= 0, K > 0, K % 128 == 0, each up to 2^24, K up to 2^20;
+ *               M == 0 or N == 0 is a successful no-op.
+ *   y           [M, N] output, dtype `dtype` (TERNARY_BF16, TERNARY_FP16 or
+ *               TERNARY_FP32), 16-byte aligned; must not overlap any input.
+ * x and w 16-byte, the scales 4-byte aligned.  For each block of 128 along K
+ * the products are exact and summed in fp32; x_scale * w_scale (an fp32
+ * product) multiplies the block's sum and the blocks are added in fp32, in an
+ * order that depends on M, N and K alone; y is rounded once, to nearest even.
+ * A NaN code or scale gives NaN in every output that reads it.
+ */
+int ternary_fp8_linear(const uint8_t *x, const float *x_scale, const uint8_t *w,
+                       const float *w_scale, int64_t M, int64_t N, int64_t K, void *y, int dtype,
+                       hipStream_t stream);
+
+/* What a router's logits become. */
+typedef enum { TERNARY_SCORE_SOFTMAX = 0, TERNARY_SCORE_SIGMOID = 1 } ternary_score;
+
+/* Limits of ternary_route (experts also of ternary_linear_experts, top_k of
+ * ternary_combine). */
+#define TERNARY_MAX_EXPERTS 512
+#define TERNARY_MAX_TOP_K 32
+#define TERNARY_MAX_EXPERT_GROUPS 64
+
+/*
+ * ternary_route - each token's experts, their weights, and the token slots
+ * sorted by expert.
+ *   logits      [T, E], dtype `dtype` (TERNARY_BF16, TERNARY_FP16, TERNARY_FP32),
+ *               row-major, aligned to its elements' size.
+ *   T, E        0 <= T <= 2^24, 1 <= E <= TERNARY_MAX_EXPERTS, T * top_k < 2^31.
+ *   bias        fp32 [E] added to the scores for the choice only, or NULL.
+ *   score       a ternary_score: p = softmax over the row, or 1 / (1 + exp(-l)).
+ *   groups      experts fall into `groups` runs of E / groups (E % groups == 0, at
+ *               most TERNARY_MAX_EXPERT_GROUPS); only experts of the `top_groups`
+ *               best groups may be chosen, a group's worth being the sum of its
+ *               two largest p + bias (its only one, if it has one).
+ *   top_k       1 <= top_k <= min(TERNARY_MAX_TOP_K, top_groups * E / groups).
+ *   renormalize nonzero: a token's weights are divided by their sum.
+ *   scale       multiplies the weights at the end.
+ *   ids, weights  int32 and fp32 [T, top_k] outputs: the experts with the largest
+ *               p + bias, largest first, ties to the lower index, and their p
+ *               (renormalised, scaled).
+ *   order       int32 [T * top_k] output: the slots t * top_k + j that hold an expert,
+ *               sorted by it (those of one expert ascending); -1 from
+ *               offsets[E] on.
+ *   offsets     int32 [E + 1] output: expert e's slots are order[offsets[e]] up to
+ *               order[offsets[e + 1] - 1].
+ *   slots       int32 [T, top_k] output: a slot's place in `order`, -1 if it
+ *               holds no expert.
+ *   workspace   device memory of ternary_route_workspace(T, E) bytes, 16-byte
+ *               aligned (NULL where that is 0).  It is written before it is
+ *               read and may be reused once the call's work is done.
+ * An expert whose logit or bias is -inf or NaN in a row cannot be chosen there
+ * and has p = 0; a logit of +inf counts as the largest finite fp32 number.  A slot for which no
+ * expert is left (a padded token's row of -inf) gets id -1 and weight 0; a sum
+ * of weights of 0 is not divided by.  Scores are computed in 64 bits, so that the choice
+ * is the exact one but for scores that agree to about 1e-15.
+ */
+int ternary_route(const void *logits, int dtype, int64_t T, int64_t E, const float *bias,
+                  int score, int groups, int top_groups, int top_k, int renormalize, float scale,
+                  int32_t *ids, float *weights, int32_t *offsets, int32_t *order, int32_t *slots,
+                  void *workspace, hipStream_t stream);
+
+/* Bytes of ternary_route's workspace (0 for few tokens), or TERNARY_ERR_SHAPE. */
+int64_t ternary_route_workspace(int64_t T, int64_t E);
+
+/* Which row of x a sorted slot of ternary_linear_experts multiplies. */
+typedef enum {
+    TERNARY_ROWS_TOKENS = 0,  /* row order[r] / top_k: x holds the tokens      */
+    TERNARY_ROWS_SORTED = 1   /* row r: x holds the sorted slots themselves   */
+} ternary_rows;
+
+/*
+ * ternary_linear_experts - for each place r < offsets[E], of expert e,
+ *     y[r, n] = sum_k x[row(r), k] * q_e[n, k] * s_e(n, k)
+ * with 8-bit activations and the experts' weights as tiled ternary codes.
+ *   x, x_scale  e4m3 [x_rows, Kp] and fp32 [x_rows, Kp/128], Kp = K rounded up to a
+ *               multiple of 128 (what ternary_fp8_quantize writes).
+ *   x_rows      rows of x: at least 1; with TERNARY_ROWS_SORTED at least R.
+ *   tiled       uint8 [E, ternary_tiled_bytes(N, K)]: each expert's tiled codes.
+ *   scale       fp16 [E, N] or [E, N, K/group_size].
+ *   E, N, K     as for ternary_route and ternary_linear; K up to 2^20.
+ *   group_size  -1 (per output channel), 128 or 256.
+ *   offsets, order  of ternary_route (order is read with TERNARY_ROWS_TOKENS only,
+ *               and may be NULL otherwise).
+ *   R           places in `order` (T * top_k), R < 2^31.  Places past offsets[E] are
+ *               left as they were in y.
+ *   top_k       slots of a token, 1 .. TERNARY_MAX_TOP_K (TERNARY_ROWS_TOKENS).
+ *   y           [R, N] output, dtype `dtype` (TERNARY_BF16, TERNARY_FP16 or
+ *               TERNARY_FP32), 16-byte aligned; must not overlap any input.
+ * x and tiled 16-byte, x_scale, offsets and order 4-byte, scale 2-byte aligned.  For each block
+ * of 128 along K the products are exact and summed in fp32; sums of blocks are
+ * multiplied by their scales and added in fp32, in an order that depends on
+ * the sizes alone, and y is rounded once.  `offsets` must ascend from 0 to at most R and
+ * `order` name rows of x: entries that do not are not followed (no memory outside the
+ * arguments is touched), the outputs that they concern are unspecified.
+ */
+int ternary_linear_experts(const uint8_t *x, const float *x_scale, int64_t x_rows,
+                           const uint8_t *tiled, const uint16_t *scale, int64_t E, int64_t N,
+                           int64_t K, int64_t group_size, const int32_t *offsets,
+                           const int32_t *order, int64_t R, int top_k, int rows, void *y,
+                           int dtype, hipStream_t stream);
+
+/*
+ * ternary_combine - the weighted sum of a token's expert rows:
+ *     out[t, n] = add[t, n] + sum_j weights[t, j] * y[slots[t, j], n]
+ *   y        [R, N], dtype `dtype` (TERNARY_BF16, TERNARY_FP16, TERNARY_FP32).
+ *   weights, slots  fp32 and int32 [T, top_k] (ternary_route); a slot outside
+ *            [0, R) adds nothing (its row is not read).
+ *   add      [T, N] of the same dtype (a shared expert's output, the residual), or
+ *            NULL for none; may be `out` itself.
+ *   out      [T, N] output of the same dtype; must not overlap the other inputs.
+ * All pointers aligned to their elements' size.  Sums in fp32, add first, then j ascending, rounded once.
+ * 0 <= T <= 2^24, 0 <= N <= 2^24, R < 2^31, 1 <= top_k <= TERNARY_MAX_TOP_K.
+ */
+int ternary_combine(const void *y, int dtype, int64_t R, int64_t N, const int32_t *slots,
+                    const float *weights, int64_t T, int top_k, const void *add, void *out,
+                    hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,274 @@
+"""fp8_quantize and fp8_linear against 64-bit references, bit for bit where the arithmetic is exact."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_ref as ref
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def tl():
+    import gemm_ternary_linear_amd as tl
+    return tl
+
+
+def host(q):
+    return q.view(torch.uint8).cpu().numpy()
+
+
+def check_quantize(tl, x, block, what):
+    """x: a device tensor. Codes and scales bit for bit."""
+    say(what)
+    q, s = tl.fp8_quantize(x, block=block)
+    rq, rs = ref.quantize(x.float().cpu().numpy(), block == "tile")
+    assert q.dtype == torch.float8_e4m3fn and tuple(q.shape) == rq.shape and tuple(s.shape) == rs.shape
+    assert np.array_equal(s.cpu().numpy(), rs, equal_nan=True), what
+    # NaN is NaN under either sign
+    a = np.where(np.isnan(ref.TABLE[host(q)]), 0x7f, host(q))
+    assert np.array_equal(a, np.where(np.isnan(ref.TABLE[rq]), 0x7f, rq)), what
+
+
+@pytest.mark.parametrize("block", ["row", "tile"])
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 128), (3, 7), (5, 130), (127, 256), (128, 1000), (129, 384), (300, 4096), (1, 18944), (1000, 136)])
+def test_quantize(tl, M, K, dtype, block):
+    rng = np.random.default_rng(M * K)
+    x = torch.from_numpy((rng.standard_normal((M, K)) * np.exp(rng.standard_normal(K))).astype(np.float32)).to(DT[dtype]).cuda()
+    check_quantize(tl, x, block, f"quantize {block} {dtype} {M}x{K}")
+
+
+@pytest.mark.parametrize("block", ["row", "tile"])
+def test_quantize_edges(tl, block):
+    """Ties, zeros, the smallest and largest numbers, infinities and NaN, each in blocks of its own row."""
+    x = np.zeros((10, 256), np.float32)
+    x[0, :16] = np.arange(16) + 0.5            # amax 448: quotients on ties
+    x[0, 20] = 448
+    x[1, :] = -0.0
+    x[2, :8] = [1e-44, -1e-44, 3e-45, 0, 1e-40, -1e-40, 1e-39, 2e-38]
+    x[2, 130:134] = [1e-45, 0, 0, -1e-45]      # its scale is rounded to 0
+    x[2, 140:142] = [2e-43, 1e-43]
+    x[3, :4] = [3.4028235e38, -3.4028235e38, 1, 1e38]
+    x[4, :4] = [np.inf, 1, -np.inf, 0]
+    x[5, :4] = [np.nan, 1, -2, 0]
+    x[6, 128:] = np.nan
+    x[7, 100] = -7                             # 448 / 7 = 64: the grid falls on whole numbers
+    x[7, :100] = np.arange(100) / 16
+    x[8, 3] = 65504
+    x[9] = np.linspace(-1, 1, 256)
+    xt = torch.from_numpy(x).cuda()
+    if block == "row":
+        check_quantize(tl, xt, "row", "edges")
+        check_quantize(tl, xt.to(torch.bfloat16), "row", "edges bf16")
+    for i in range(10):
+        check_quantize(tl, xt[i:i + 1].contiguous(), block, f"edge row {i}")
+
+
+def test_quantize_strides_and_alignment(tl):
+    rng = np.random.default_rng(8)
+    big = torch.from_numpy(rng.standard_normal((70, 1100)).astype(np.float32)).to(torch.bfloat16).cuda()
+    for a, b in [(0, 1024), (8, 264), (1, 257), (3, 1100), (96, 97)]:
+        check_quantize(tl, big[:, a:b], "row", f"columns {a}:{b}")
+        check_quantize(tl, big[:, a:b], "tile", f"columns {a}:{b}")
+    check_quantize(tl, big[::7, 16:272], "row", "every seventh row")
+    with pytest.raises(ValueError):
+        tl.fp8_quantize(big.t())
+    with pytest.raises(ValueError):
+        tl.fp8_quantize(big[:1].expand(5, 1100))
+
+
+def test_quantize_far_rows(tl):
+    """Rows more than 2^31 elements apart."""
+    say("far rows")
+    ld = (1 << 31) + 8
+    buf = torch.zeros(ld + 512, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((2, 512), (ld, 1))
+    x.copy_(torch.linspace(-3, 5, 1024).view(2, 512))
+    check_quantize(tl, x, "row", "far rows")
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M,K", [(1, 128), (7, 100), (33, 1024), (64, 2050), (2, 1)])
+def test_quantize_swiglu(tl, M, K, dtype):
+    say(f"swiglu {dtype} {M}x{K}")
+    rng = np.random.default_rng(M + K)
+    x = torch.from_numpy((3 * rng.standard_normal((M, 2 * K))).astype(np.float32)).to(DT[dtype]).cuda()
+    x[0, 0] = -200.0  # silu underflows to -0
+    q, s = tl.fp8_quantize(x, act="swiglu")
+    w = x.double().cpu().numpy()
+    v = w[:, :K] / (1 + np.exp(-w[:, :K])) * w[:, K:]
+    kb = ref.up(K, 128) // 128
+    v = np.pad(v, ((0, 0), (0, kb * 128 - K)))
+    big = np.abs(v.reshape(M, kb, 128)).max(2)
+    s = s.cpu().numpy().astype(np.float64)
+    # v: exp of a 32-bit product (its relative error grows with |gate|, at most 20 here: 20 x 2^-23), a sum, a
+    # division and a product: under 2^-18 in all; s: that, a division's 2^-24
+    assert np.all(np.abs(s - big / 448) <= 2.0 ** -17 * big / 448 + 1e-44)
+    d = np.repeat(s, 128, 1)
+    t = np.where(d > 0, v / np.where(d > 0, d, 1), 0)
+    step = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(t), 2.0 ** -6))) - 3)
+    assert np.all(np.abs(ref.TABLE[host(q)] - t) <= step / 2 + 2.0 ** -17 * np.abs(t) + 1e-30)
+    assert not host(q)[:, K:].any()
+
+
+def linear_case(rng, M, N, K, exact):
+    if exact:
+        return (ref.codes_of(rng, M, K), ref.scales_of(rng, M, K // 128), ref.codes_of(rng, N, K),
+                ref.scales_of(rng, (N + 127) // 128, K // 128))
+    xq, xs = ref.quantize((rng.standard_normal((M, K)) * np.exp(0.7 * rng.standard_normal(K))).astype(np.float32), False)
+    wq, ws = ref.quantize((0.02 * rng.standard_normal((N, K))).astype(np.float32), True)
+    return xq, xs, wq, ws
+
+
+def run_linear(tl, xq, xs, wq, ws, dtype, **kw):
+    return tl.fp8_linear(ref.fp8_dev(xq), ref.dev(xs), ref.fp8_dev(wq), ref.dev(ws), dtype=dtype, **kw)
+
+
+SHAPES = [(1, 16, 128), (1, 1, 128), (1, 4096, 4096), (2, 17, 256), (3, 130, 384), (8, 512, 1024), (15, 1000, 640), (16, 128, 8192),
+          (17, 257, 512), (31, 4100, 256), (32, 256, 1280), (33, 129, 128), (45, 1024, 2048), (64, 200, 896), (65, 255, 384), (100, 64, 4096),
+          (127, 128, 256), (128, 384, 512), (129, 100, 1152), (200, 513, 384), (256, 256, 128), (257, 260, 256), (300, 1000, 640), (511, 127, 1664),
+          (700, 1030, 256), (1025, 300, 384), (2048, 2304, 256), (4100, 36, 128)]
+
+
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_linear_exact(tl, M, N, K):
+    """Whole-number codes and scales that are powers of two: fp32 sums are exact, every output bit is known."""
+    say(f"linear exact {M} {N} {K}")
+    xq, xs, wq, ws = linear_case(np.random.default_rng(M * 7 + N + K), M, N, K, True)
+    y = ref.wide(xq, xs) @ ref.wide(wq, ws, 128).T
+    # 64 products of |8 x 8| x 16 and steps of 1/16: below 2^24 steps up to K = 1024 in the worst case, and in
+    # these draws (random signs) at every K here
+    assert np.abs(ref.wide(xq, xs)).max() <= 32 and np.abs(y).max() < 2.0 ** 19
+    for name, dt in DT.items():
+        got = run_linear(tl, xq, xs, wq, ws, dt)
+        assert got.dtype == dt and np.array_equal(got.double().cpu().numpy(), ref.rounded(y, dt)), name
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("M,N,K", [(1, 512, 4096), (5, 300, 1152), (24, 260, 8192), (70, 144, 2048), (200, 400, 1024), (600, 515, 640)])
+def test_linear(tl, M, N, K, dtype):
+    say(f"linear {dtype} {M} {N} {K}")
+    xq, xs, wq, ws = linear_case(np.random.default_rng(M + N + K), M, N, K, False)
+    xw, ww = ref.wide(xq, xs), ref.wide(wq, ws, 128)
+    y = xw @ ww.T
+    got = run_linear(tl, xq, xs, wq, ws, DT[dtype])
+    assert np.all(np.abs(got.double().cpu().numpy() - y) <= ref.product_bound(xw, ww, K // 128, DT[dtype], y))
+    assert torch.equal(got, run_linear(tl, xq, xs, wq, ws, DT[dtype])), "the same inputs give the same bits"
+
+
+@pytest.mark.parametrize("M", [1, 20, 150, 600])
+def test_linear_nan(tl, M):
+    """A NaN code or scale shows in the outputs that read it, and in no other."""
+    say(f"linear NaN M={M}")
+    N, K = 384, 512
+    xq, xs, wq, ws = linear_case(np.random.default_rng(M), M, N, K, True)
+    xq[M // 2, 77], wq[N - 1, 300], ws[0, 1] = 0x7f, 0xff, np.inf
+    xs[M - 1, 3] = np.nan
+    with np.errstate(all="ignore"):
+        xw, ww = ref.wide(xq, xs), ref.wide(wq, ws, 128)
+        nan = np.isnan(xw).any(1)[:, None] | (~np.isfinite(ww)).any(1)[None, :]
+    got = run_linear(tl, xq, xs, wq, ws, torch.float32).cpu().numpy()
+    assert not np.isfinite(got[nan]).any()
+    keep_m, keep_n = ~np.isnan(xw).any(1), np.isfinite(ww).all(1)
+    assert np.array_equal(got[np.ix_(keep_m, keep_n)], xw[keep_m] @ ww[keep_n].T)
+
+
+def test_linear_out_and_bounds(tl):
+    """`out` is written whole and nothing beside it; views of larger buffers serve as inputs."""
+    say("linear out")
+    rng = np.random.default_rng(3)
+    for M, N, K in [(5, 37, 256), (40, 67, 128), (130, 131, 256), (300, 270, 384)]:
+        xq, xs, wq, ws = linear_case(rng, M, N, K, True)
+        y = ref.wide(xq, xs) @ ref.wide(wq, ws, 128).T
+        for dt in DT.values():
+            buf = torch.full((M * N + 64,), 77.0, dtype=dt, device="cuda")
+            out = buf[32:32 + M * N].view(M, N)
+            r = run_linear(tl, xq, xs, wq, ws, dt, out=out)
+            assert r is out and np.array_equal(out.double().cpu().numpy(), ref.rounded(y, dt))
+            assert bool((buf[:32] == 77).all()) and bool((buf[32 + M * N:] == 77).all())
+        # rows past the inputs' last hold NaN codes: none may show
+        more = ref.fp8_dev(np.vstack([xq, np.full((300, K), 0x7f, np.uint8)]))[:M]
+        wore = ref.fp8_dev(np.vstack([wq, np.full((300, K), 0x7f, np.uint8)]))[:N]
+        got = tl.fp8_linear(more, ref.dev(xs), wore, ref.dev(ws), dtype=torch.float32)
+        assert np.array_equal(got.cpu().numpy(), y)
+    with pytest.raises(ValueError):
+        tl.fp8_linear(more, ref.dev(xs), wore, ref.dev(ws), out=torch.empty(M, N + 1, device="cuda"))
+    assert tuple(tl.fp8_linear(more[:0], ref.dev(xs)[:0], wore, ref.dev(ws)).shape) == (0, N)
+
+
+@pytest.mark.parametrize("M,N,K", [((1 << 17) + 3, 16400, 128), (70001, 16, 256), (1, 1 << 20, 128)])
+def test_linear_far(tl, M, N, K):
+    """Outputs past 2^31 elements; many row tiles; many channel tiles. Sampled rows and columns."""
+    say(f"linear far {M} {N} {K}")
+    g = torch.Generator(device="cuda").manual_seed(M)
+    def codes(n):
+        return torch.randint(-8, 9, (n, K), generator=g, device="cuda").float().to(torch.float8_e4m3fn)
+    x, w = codes(M), codes(N)
+    xs = torch.exp2(torch.randint(-2, 3, (M, K // 128), generator=g, device="cuda").float())
+    ws = torch.exp2(torch.randint(-2, 3, ((N + 127) // 128, K // 128), generator=g, device="cuda").float())
+    y = tl.fp8_linear(x, xs, w, ws, dtype=torch.float16)
+    rows = torch.tensor(sorted({0, 1, M // 3, M // 2, M - 129, M - 2, M - 1} & set(range(M))), device="cuda")
+    cols = torch.tensor(sorted({0, 5, N // 2, N - 17, N - 1} & set(range(N))), device="cuda")
+    xw = x[rows].float().double() * xs[rows].double().repeat_interleave(128, 1)
+    ww = w.float() * ws.repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)
+    full = (xw.float() @ ww.t().contiguous()).to(torch.float16)  # exact in 32 bits, as above
+    assert torch.equal(y[rows], full)
+    part = ww[cols].double() @ (x.float() * xs.repeat_interleave(128, 1)).double().t().contiguous()
+    assert torch.equal(y[:, cols], part.t().float().to(torch.float16))
+
+
+def test_quantized_layer(tl):
+    """Quantise both sides on the GPU, multiply: against the unquantised product, within what 8 bits cost."""
+    say("quantised layer")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, w = torch.randn(50, 1000, generator=g, device="cuda"), 0.05 * torch.randn(300, 1000, generator=g, device="cuda")
+    xq, xs = tl.fp8_quantize(x.to(torch.bfloat16))
+    wq, ws = tl.fp8_quantize(w.to(torch.float16), block="tile")
+    y = tl.fp8_linear(xq, xs, wq, ws, dtype=torch.float32)
+    true = x.double() @ w.double().t().contiguous()
+    # each factor within 2^-4 of itself (and the 16-bit rounding): products within 2^-3 + 2^-7; errors that add
+    # up at most linearly
+    assert bool(((y.double() - true).abs() <= (2.0 ** -3 + 2.0 ** -7) * (x.abs().double() @ w.abs().double().t().contiguous())
+                 + 1000 * 448 * 2.0 ** -10 * (xs.max() * ws.max()).double() * 448).all())
+    assert float((y.double() - true).norm() / true.norm()) < 2.0 ** -4
+
+
+def test_capture_and_streams(tl):
+    """Captured and replayed several times, with eager work between, and on two streams at once."""
+    say("capture")
+    rng = np.random.default_rng(11)
+    cases = [(1, 512, 1024), (40, 300, 512), (300, 520, 384)]
+    ins = []
+    for c in cases:
+        xq, xs, wq, ws = linear_case(rng, *c, True)
+        ins.append([ref.fp8_dev(xq), ref.dev(xs), ref.fp8_dev(wq), ref.dev(ws)])
+    x = torch.randn(40, 1024, device="cuda")
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        outs = [tl.fp8_linear(*i) for i in ins]
+        q, s = tl.fp8_quantize(x)
+    for rep in range(4):
+        for i in ins:
+            i[0].copy_(ref.fp8_dev(ref.codes_of(rng, *i[0].shape)))
+        x.normal_()
+        gr.replay()
+        torch.cuda.synchronize()
+        for i, o in zip(ins, outs):
+            assert torch.equal(o, tl.fp8_linear(*i)), rep
+        eq, es = tl.fp8_quantize(x)
+        assert torch.equal(q.view(torch.uint8), eq.view(torch.uint8)) and torch.equal(s, es)
+    want = [tl.fp8_linear(*i) for i in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for rep in range(20):
+        for k, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[k].append([tl.fp8_linear(*i) for i in ins])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for side in got for r in side for a, b in zip(r, want))
