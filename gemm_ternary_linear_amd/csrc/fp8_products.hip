@@ -93,6 +93,22 @@ __device__ __forceinline__ i32x8_v join(u32x4_v a, u32x4_v b)
     return i32x8_v{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
 }
 
+// Four channels ch .. ch + 3 of a row of y (those past N are left out).
+template <int DT>
+__device__ __forceinline__ void put4(const Fp8Product &p, int row, int ch, f32x4_t s)
+{
+    const int64_t at = (int64_t)row * p.N + ch;
+    if (p.N % 4 == 0) {
+        if (ch < p.N)
+            store4<DT>(p.y, at, s);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (ch + i < p.N)
+                store_elem<DT>(p.y, at + i, s[i]);
+    }
+}
+
 constexpr int kWaves = 4, kThreads = kWaves * 64;
 
 // A workgroup computes 16 channels x 16 MT rows; its waves share the K blocks
@@ -192,16 +208,7 @@ __global__ void __launch_bounds__(kThreads) stream_kernel(const Fp8Product p)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     s[i] *= f16_bits_to_f32(p.t_scale[(int64_t)e * p.N + min(ch + i, p.N - 1)]);
-        const int64_t at = (int64_t)row * p.N + ch;
-        if (p.N % 4 == 0) {
-            if (ch < p.N)
-                store4<DT>(p.y, at, s);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (ch + i < p.N)
-                    store_elem<DT>(p.y, at + i, s[i]);
-        }
+        put4<DT>(p, row, ch, s);
     }
 }
 
@@ -212,6 +219,353 @@ hipError_t launch_stream(const Fp8Product &p, int64_t tiles, hipStream_t stream)
     with_dtype(p.dtype, [&](auto dt) {
         hipLaunchKernelGGL((stream_kernel<TERN, MT, decltype(dt)::value>), dim3(nx, (unsigned)tiles),
                            dim3(kThreads), 0, stream, p);
+    });
+    return hipGetLastError();
+}
+
+// ---------------------------------------------------------------- many rows
+
+// s_waitcnt for vector memory alone (gfx9 encoding), then the workgroup's barrier.
+template <int N>
+__device__ __forceinline__ void wait_and_barrier()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    asm volatile("s_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+typedef __attribute__((address_space(3))) u32x4_v lds_u4;
+typedef __attribute__((address_space(3))) u32x2_v lds_u2;
+typedef __attribute__((address_space(3))) void lds_void;
+
+// One memory-to-LDS load: 16 bytes a lane from `src`, to lds + 16 * lane.
+__device__ __forceinline__ void load_to_lds(const uint8_t *src, lds_u4 *lds)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)src,
+                                     (lds_void *)lds, 16, 0, 0);
+#endif
+}
+
+// The same from a buffer resource.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t rsrc, lds_u4 *lds, int voff, int soff)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_void *)lds, 16, voff, soff,
+                                             0, 0);
+#endif
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000);
+}
+
+// A row of a stage is 128 bytes, eight chunks of 16; chunk c of row r sits at
+// c ^ swz(r), which spreads the rows that a fragment read touches over the banks.
+__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+
+template <int TN_, int TM_, int WN_, int WM_>
+struct Tile {
+    static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_;
+    static constexpr int THREADS = WN * WM * 64;
+    static constexpr int FN = TN / WN / 16, FM = TM / WM / 16;  // fragments of a wave
+};
+
+// weights' scales are read by scalar loads: the same for a whole workgroup
+typedef const __attribute__((address_space(4))) float constant_float;
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+
+// Values b0 .. b0 + 3 of a row of n (unspecified past its end).
+__device__ __forceinline__ f32x4_t load_scales(const float *row, int b0, int n)
+{
+    if (n < 4) {
+        return f32x4_t{row[min(b0, n - 1)], row[min(b0 + 1, n - 1)], row[min(b0 + 2, n - 1)], row[n - 1]};
+    }
+    // the row's last four at its end, moved down
+    const int at = min(b0, n - 4);
+    f32x4_u u = *reinterpret_cast<const f32x4_u *>(row + at);
+    if (at + 1 <= b0)
+        u = u.yzww;
+    if (at + 2 <= b0)
+        u = u.yzww;
+    if (at + 3 <= b0)
+        u = u.yzww;
+    return f32x4_t{u.x, u.y, u.z, u.w};
+}
+// The same for a row that a whole workgroup reads (scalar loads).
+__device__ __forceinline__ f32x4_t load_scales_uniform(const float *row, int b0, int n)
+{
+    constant_float *r = (constant_float *)row;
+    return f32x4_t{r[min(b0, n - 1)], r[min(b0 + 1, n - 1)], r[min(b0 + 2, n - 1)], r[min(b0 + 3, n - 1)]};
+}
+
+// G: group-scaled ternary weights.
+template <bool TERN, bool G, int DT, class C>
+__global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
+{
+    constexpr int TN = C::TN, TM = C::TM, FN = C::FN, FM = C::FM, THREADS = C::THREADS;
+    constexpr int XI = TM * 8 / THREADS;                      // x loads of a thread and stage
+    constexpr int WCH = TERN ? TN * 2 : TN * 8;               // 16-byte chunks of w in a stage
+    constexpr int WI = (WCH + THREADS - 1) / THREADS;
+    constexpr int QB = TERN ? 1 : (TN + 127) / 128;           // blocks of channels with scales of their own
+    static_assert(TM * 8 % THREADS == 0 && (WCH % THREADS == 0 || WI == 1) && TM <= THREADS && TN <= THREADS);
+    // one object per stage: a load into one stage is then known not to touch the other
+    __shared__ __attribute__((aligned(16))) u32x4_v sx0[TM * 8], sx1[TM * 8], sw0[WCH], sw1[WCH];
+    // scales of eight steps: x's (times w's for 8-bit weights), a lane's FM
+    // rows together, and a group's channels'.  Each is read by one load: a pair of loads that the
+    // compiler merges loses the object it reads, and with it would wait for every stage in flight.
+    typedef float fm_t __attribute__((ext_vector_type(FM)));
+    __shared__ __attribute__((aligned(16))) fm_t sf[QB][8][TM / FM];
+    __shared__ __attribute__((aligned(16))) f32x4_t sg[G ? 8 : 1][G ? TN / 4 : 1];
+
+    lds_u4 *const lx[2] = {(lds_u4 *)sx0, (lds_u4 *)sx1}, *const lw[2] = {(lds_u4 *)sw0, (lds_u4 *)sw1};
+
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % C::WN, wm = wave / C::WN;
+    const int nb = p.nb;
+    const int ntn = (p.N + TN - 1) / TN;
+    const int tm = blockIdx.x / ntn, tn = blockIdx.x % ntn;
+    const int n0 = tn * TN;
+    // dense: the last tile ends at M, so that every row of a tile exists (rows of
+    // two tiles are computed by both, to the same bits)
+    int e = 0, r0 = min(tm * TM, p.M - TM), r1 = r0 + TM;
+    if constexpr (TERN)
+        if (!find_tile<TM>(p.offsets, p.E, p.M, tm, e, r0, r1))
+            return;
+
+    auto x_row = [&](int r) -> int64_t {  // row of x of the tile's row r
+        int64_t row = min(r0 + r, r1 - 1);
+        if constexpr (TERN) {
+            if (p.order)
+                row = p.order[row] / p.top_k;
+            row = row < 0 || row >= p.x_rows ? 0 : row;
+        }
+        return row;
+    };
+    // Sources.  Gathered rows of x and the experts' blocks have pointers of
+    // their own; a dense tile is one resource, each thread's rows a uniform
+    // distance apart.
+    constexpr int RS = THREADS / 8;        // rows between a thread's chunks of x
+    const int rowbytes = nb * kFp8Block;   // at most 2^20
+    static_assert(RS % 16 == 0, "the same chunk of each row");
+    const uint8_t *xsrc[XI], *wsrc = nullptr;
+    int woff[WI];
+    const int off = (tid >> 3) * rowbytes + 16 * ((tid & 7) ^ swz(tid >> 3));
+    __amdgpu_buffer_rsrc_t xr, wr;
+    if constexpr (TERN) {
+#pragma unroll
+        for (int i = 0; i < XI; ++i)
+            xsrc[i] = p.x + x_row((tid >> 3) + i * RS) * rowbytes + 16 * ((tid & 7) ^ swz(tid >> 3));
+        // 32 chunks of a block of 16 channels are a half slab, consecutive in memory
+        static_assert(!TERN || WI == 1);
+        const int blk = min(n0 / 16 + (tid >> 5), (p.N + 15) / 16 - 1);
+        wsrc = p.w + ((int64_t)e * ((p.N + 15) / 16) + blk) * ((nb + 1) / 2) * kTileBytes + 16 * (tid & 31);
+    } else {
+        xr = make_rsrc(p.x + (int64_t)r0 * rowbytes, (uint32_t)(TM * rowbytes));
+        const int chans = min(TN, p.N - n0);  // (those past the last repeat it)
+        wr = make_rsrc(p.w + (int64_t)n0 * rowbytes, (uint32_t)(chans * rowbytes));
+#pragma unroll
+        for (int i = 0; i < WI; ++i)
+            woff[i] = min((tid >> 3) + i * RS, chans - 1) * rowbytes + 16 * ((tid & 7) ^ swz(tid >> 3));
+    }
+    const float *fsrc = p.x_scale + (tid < TM ? x_row(tid) : 0) * nb;
+    const uint16_t *gsrc = G ? p.t_scale + ((int64_t)e * p.N + min(n0 + tid, p.N - 1)) * p.ngroups : nullptr;
+    const int gsteps = G ? p.group / kFp8Block : 1;
+
+    auto issue = [&](auto S, int b) {
+        constexpr int s = decltype(S)::value;
+#pragma unroll
+        for (int i = 0; i < XI; ++i) {
+            lds_u4 *to = lx[s] + i * THREADS + wave * 64;
+            if constexpr (TERN)
+                load_to_lds(xsrc[i] + b * kFp8Block, to);
+            else
+                load_to_lds(xr, to, off, i * RS * rowbytes + b * kFp8Block);
+        }
+#pragma unroll
+        for (int i = 0; i < WI; ++i) {
+            lds_u4 *to = lw[s] + i * THREADS + wave * 64;
+            if constexpr (!TERN)
+                load_to_lds(wr, to, woff[i], b * kFp8Block);
+            else if (WCH % THREADS == 0 || wave * 64 < WCH)
+                load_to_lds(wsrc + (int64_t)b * (kTileBytes / 2), to);
+        }
+    };
+    f32x4_t fx = {0.f, 0.f, 0.f, 0.f}, fw[QB], gv = fx;
+    auto load_factors = [&](int b0) {  // of steps b0 .. b0 + 3
+        if (wave < TM / 64)
+            fx = load_scales(fsrc, b0, nb);
+        if constexpr (!TERN)
+#pragma unroll
+            for (int q = 0; q < QB; ++q)
+                fw[q] = load_scales_uniform(p.w_scale + (int64_t)min(n0 / 128 + q, (p.N - 1) / 128) * nb, b0, nb);
+        if constexpr (G)
+            if (wave < TN / 64)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    gv[i] = f16_bits_to_f32(gsrc[min(b0 + i, nb - 1) / gsteps]);
+    };
+    // row r = 16 (FM u + j) + c of the tile: entry j of (u, c)
+    const int fpos = ((tid / (16 * FM)) * 16 + (tid & 15)) * FM + (tid >> 4) % FM;
+    auto store_factors = [&](int b0) {
+        if (wave < TM / 64)
+#pragma unroll
+            for (int q = 0; q < QB; ++q)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<float *>(sf[q][(b0 + i) & 7])[fpos] = TERN ? fx[i] : fx[i] * fw[q][i];
+        if constexpr (G)
+            if (wave < TN / 64)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<float *>(sg[(b0 + i) & 7])[tid] = gv[i];
+    };
+
+    f32x4_t acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+            acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    // Chunks of a row that lane group g holds: g and g + 4.  Ternary: the codes of
+    // two fragments come by one load, 16 bytes of the first fragment's in lanes 0 .. 31, of the
+    // second's in the others; exchanging the halves of each (permlane32_swap)
+    // leaves a fragment with the codes 0, 64, 32 and 96 (and 31 more) in its lane
+    // groups, so x's chunks are 0, 1, 4, 5 and those two further on.
+    static_assert(!TERN || FN % 2 == 0);
+    const int xa = (wm * FM * 16 + col) * 8, cg = TERN ? g + (g & 2) : g;
+    const int c0 = cg ^ swz(col), c1 = (cg + (TERN ? 2 : 4)) ^ swz(col);
+    const int wa = TERN ? wn * FN * 32 + lane : (wn * FN * 16 + col) * 8;
+
+    auto compute = [&](auto S, int b) {
+        constexpr int s = decltype(S)::value;
+        // Raw operand of fragment i (ternary: of i and i + 1), read ahead.
+        struct Raw {
+            u32x4_v a, b;
+        };
+        auto read_w = [&](int i) -> Raw {
+            Raw r = {};
+            if constexpr (TERN) {
+                r.a = lw[s][wa + i * 32];
+            } else {
+                r.a = lw[s][wa + i * 128 + c0];
+                r.b = lw[s][wa + i * 128 + c1];
+            }
+            return r;
+        };
+        u32x2_v next_codes = {0, 0};
+        auto operand = [&](const Raw &r, int i) -> i32x8_v {
+            if constexpr (TERN) {
+                u32x2_v w = next_codes;
+                if (i % 2 == 0) {
+                    const u32x2_v lo = __builtin_amdgcn_permlane32_swap(r.a.x, r.a.z, false, false);
+                    const u32x2_v hi = __builtin_amdgcn_permlane32_swap(r.a.y, r.a.w, false, false);
+                    w = u32x2_v{lo.x, hi.x};
+                    next_codes = u32x2_v{lo.y, hi.y};
+                }
+                int d[4];
+                codes_to_fp4(w.x, d[0], d[1]);
+                codes_to_fp4(w.y, d[2], d[3]);
+                return i32x8_v{d[0], d[1], d[2], d[3], 0, 0, 0, 0};
+            } else {
+                return join(r.a, r.b);
+            }
+        };
+        i32x8_v xf[FM];
+        Raw raw = read_w(0);
+        const fm_t f = sf[TERN ? 0 : (wn * FN * 16) / 128][b & 7][wm * 16 + col];
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const u32x4_v a = lx[s][xa + j * 128 + c0], c = lx[s][xa + j * 128 + c1];
+            xf[j] = TERN ? odd_even(a, c) : join(a, c);
+        }
+        // Each matrix instruction is followed by the scaling of a result of the
+        // fragment before, so that neither waits for the other.
+        f32x4_t d[2][FM], gs[2];
+#pragma unroll
+        for (int i = 0; i <= FN; ++i) {
+            const i32x8_v a = i < FN ? operand(raw, i) : i32x8_v{};
+            if (TERN ? i % 2 == 0 && i + 2 < FN : i + 1 < FN)
+                raw = read_w(TERN ? i + 2 : i + 1);
+            if constexpr (G)
+                if (i < FN)
+                    gs[i & 1] = sg[b & 7][(wn * FN + i) * 4 + g];
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                if (i < FN)
+                    d[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        a, xf[j], zero, TERN ? kFp4 : kFp8, kFp8, 0, TERN ? kHalf : kOne, 0, kOne);
+                if (i > 0)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[i > 0 ? i - 1 : 0][j][k] += d[(i & 1) ^ 1][j][k] * (G ? f[j] * gs[(i & 1) ^ 1][k] : f[j]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+
+    load_factors(0);
+    store_factors(0);
+    issue(std::integral_constant<int, 0>(), 0);
+    // the factors of steps 0 .. 3 must be in LDS before the first barrier is passed
+    __builtin_amdgcn_s_waitcnt(0);
+    // Every step loads the next one's stage (the last loads itself again, into
+    // a stage that is not read: a branch there had the compiler copy the step, and
+    // so did a second exit of the loop).
+    int b = 0;
+    for (; b + 1 < nb; b += 2) {
+        wait_and_barrier<0>();
+        issue(std::integral_constant<int, 1>(), b + 1);
+        // scales of the steps ahead: loaded at the first of four, put into LDS at the third
+        if (b & 2)
+            store_factors(b + 2);
+        else
+            load_factors(b + 4);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(std::integral_constant<int, 0>(), b);
+        wait_and_barrier<0>();
+        issue(std::integral_constant<int, 0>(), min(b + 2, nb - 1));
+        __builtin_amdgcn_sched_barrier(0);
+        compute(std::integral_constant<int, 1>(), b + 1);
+    }
+    wait_and_barrier<0>();
+    if (b < nb)
+        compute(std::integral_constant<int, 0>(), b);
+
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+        const int ch = n0 + (wn * FN + i) * 16 + 4 * g;
+        f32x4_t cs = {1.f, 1.f, 1.f, 1.f};
+        if constexpr (TERN && !G)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                cs[k] = f16_bits_to_f32(p.t_scale[(int64_t)e * p.N + min(ch + k, p.N - 1)]);
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int row = r0 + (wm * FM + j) * 16 + col;
+            if (row < r1)
+                put4<DT>(p, row, ch, TERN && !G ? acc[i][j] * cs : acc[i][j]);
+        }
+    }
+}
+
+template <bool TERN, class C>
+hipError_t launch_tiles(const Fp8Product &p, int64_t tiles, hipStream_t stream)
+{
+    const int64_t wgs = tiles * ((p.N + C::TN - 1) / C::TN);
+    if (wgs > INT32_MAX)
+        return hipErrorInvalidValue;
+    with_dtype(p.dtype, [&](auto dt) {
+        constexpr int DT = decltype(dt)::value;
+        if (TERN && p.group)
+            hipLaunchKernelGGL((tile_kernel<TERN, TERN, DT, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
+        else
+            hipLaunchKernelGGL((tile_kernel<TERN, false, DT, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
     });
     return hipGetLastError();
 }
@@ -228,14 +582,18 @@ hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
 {
     if (p.M <= 16)
         return launch_stream<false, 1>(p, 1, stream);
-    return launch_stream<false, 4>(p, (p.M + 63) / 64, stream);
+    if (p.M < 256)
+        return launch_stream<false, 4>(p, (p.M + 63) / 64, stream);
+    return launch_tiles<false, Tile<256, 256, 2, 4>>(p, (p.M + 255) / 256, stream);
 }
 
 hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream)
 {
     if (p.M <= 16 * p.E)
         return launch_stream<true, 1>(p, expert_tiles(p, 16), stream);
-    return launch_stream<true, 4>(p, expert_tiles(p, 64), stream);
+    if (p.M <= 32 * p.E)
+        return launch_stream<true, 4>(p, expert_tiles(p, 64), stream);
+    return launch_tiles<true, Tile<256, 256, 2, 4>>(p, expert_tiles(p, 256), stream);
 }
 
 }  // namespace ternary
