@@ -7,8 +7,7 @@
 // by 16 rows of x (B) over one block of 128; its fp32 sums are then scaled and
 // added to the running sums, so no rounding but fp32's happens before the end.
 // A lane's four results are four channels of one row: the row's scale is one
-// register and the four go out in one store.  Ternary codes become fp4 (+-2,
-// halved by the instruction's A scale) in five vector operations a 16 codes;
+// register and the four go out in one store.  Ternary codes become fp4 (+-2) in five vector operations a 16 codes;
 // as those give a word's odd codes, then its even ones, x's bytes are put in the
 // same order (eight byte permutes per 16 rows x 128).  Lane group g (lanes 16 g
 // up) holds k = 32 g .. 32 g + 31 of a block of an fp4 operand, and k = 16 g .. and
@@ -20,8 +19,18 @@ namespace ternary {
 
 namespace {
 
-constexpr int kFp8 = 0, kFp4 = 4;      // operand types of the matrix instruction
-constexpr int kOne = 127, kHalf = 126;  // its E8M0 scales
+// One block of 128: 16 channels by 16 rows.  Without the instruction's own block
+// scales (both arguments 0) it issues faster: in a loop with the scaling of its results,
+// 4480 against 3883 TFLOP/s.  So an fp4 operand's +-2 stay, and half of each is left to
+// the channel's scale.
+template <bool TERN>
+__device__ __forceinline__ f32x4_t mfma(i32x8_v w, i32x8_v x)
+{
+    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, TERN ? 4 : 0, 0, 0, 0, 0, 0);
+}
+// Scale of a channel's fp4 products.
+__device__ __forceinline__ float channel_scale(uint16_t s) { return 0.5f * f16_bits_to_f32(s); }
 
 // Places [r0, r1) of expert e that the idx-th tile of BM rows covers (tiles run
 // expert by expert); false past the last.  Every lane of a wave calls it.
@@ -150,7 +159,6 @@ __global__ void __launch_bounds__(kThreads) stream_kernel(const Fp8Product p)
 #pragma unroll
     for (int j = 0; j < MT; ++j)
         acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
 
     for (int b = wave; b < nb; b += kWaves) {
         i32x8_v a;
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(kThreads) stream_kernel(const Fp8Product p)
                 const int gi = (int)((int64_t)b * kFp8Block / p.group);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    ws[i] = f16_bits_to_f32(
+                    ws[i] = channel_scale(
                         p.t_scale[((int64_t)e * p.N + min(n0 + 4 * g + i, p.N - 1)) * p.ngroups + gi]);
             }
         } else {
@@ -181,11 +189,9 @@ __global__ void __launch_bounds__(kThreads) stream_kernel(const Fp8Product p)
             const float xs = sp[j][b];
             f32x4_t d;
             if constexpr (TERN)
-                d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    a, odd_even(xv[0], xv[4]), zero, kFp4, kFp8, 0, kHalf, 0, kOne);
+                d = mfma<true>(a, odd_even(xv[0], xv[4]));
             else
-                d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, join(xv[0], xv[4]), zero, kFp8,
-                                                                     kFp8, 0, kOne, 0, kOne);
+                d = mfma<false>(a, join(xv[0], xv[4]));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 acc[j][i] += d[i] * (TERN ? xs * ws[i] : xs * ws[0]);
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) stream_kernel(const Fp8Product p)
             if (!p.group)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    s[i] *= f16_bits_to_f32(p.t_scale[(int64_t)e * p.N + min(ch + i, p.N - 1)]);
+                    s[i] *= channel_scale(p.t_scale[(int64_t)e * p.N + min(ch + i, p.N - 1)]);
         put4<DT>(p, row, ch, s);
     }
 }
@@ -225,12 +231,12 @@ hipError_t launch_stream(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 
 // ---------------------------------------------------------------- many rows
 
-// s_waitcnt for vector memory alone (gfx9 encoding), then the workgroup's barrier.
-template <int N>
-__device__ __forceinline__ void wait_and_barrier()
+// Waits for everything this wave has loaded (LDS reads, and loads into LDS among
+// them), then for the workgroup's other waves.
+__device__ __forceinline__ void meet()
 {
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+    __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
     asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
@@ -264,7 +270,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, ui
 
 // A row of a stage is 128 bytes, eight chunks of 16; chunk c of row r sits at
 // c ^ swz(r), which spreads the rows that a fragment read touches over the banks.
-__device__ __forceinline__ int swz(int r) { return (r & 7) ^ ((r >> 3) & 1); }
+__device__ __forceinline__ int swz(int r) { return r & 7; }
 
 template <int TN_, int TM_, int WN_, int WM_>
 struct Tile {
@@ -326,8 +332,28 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wn = wave % C::WN, wm = wave / C::WN;
     const int nb = p.nb;
+    // Workgroup b runs on XCD b % 8 (each has an L2 of its own).  Dense: an XCD takes a
+    // run of tiles, eight row tiles of a channel tile after the other, so that its 32 or
+    // so workgroups at a time share 8 x tiles and a few w tiles, and w is read by one XCD
+    // per eight row tiles.  Experts: it takes every eighth row tile (how many there are is only known
+    // here), its channel tiles one after the other.
     const int ntn = (p.N + TN - 1) / TN;
-    const int tm = blockIdx.x / ntn, tn = blockIdx.x % ntn;
+    const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
+    int tm, tn;
+    if constexpr (TERN) {
+        tm = slot / ntn * 8 + xcd;
+        tn = slot % ntn;
+    } else {
+        const int ntm = (p.M + TM - 1) / TM;
+        const int64_t tiles = (int64_t)ntm * ntn;
+        const int64_t t = tiles * xcd / 8 + slot;
+        if (t >= tiles * (xcd + 1) / 8)
+            return;
+        const int64_t band = (int64_t)8 * ntn;
+        const int m0 = (int)(t / band) * 8, rows = min(8, ntm - m0), in = (int)(t % band);
+        tm = m0 + in % rows;
+        tn = in / rows;
+    }
     const int n0 = tn * TN;
     // dense: the last tile ends at M, so that every row of a tile exists (rows of
     // two tiles are computed by both, to the same bits)
@@ -350,7 +376,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
     // distance apart.
     constexpr int RS = THREADS / 8;        // rows between a thread's chunks of x
     const int rowbytes = nb * kFp8Block;   // at most 2^20
-    static_assert(RS % 16 == 0, "the same chunk of each row");
+    static_assert(RS % 8 == 0, "the same chunk of each row");
     const uint8_t *xsrc[XI], *wsrc = nullptr;
     int woff[WI];
     const int off = (tid >> 3) * rowbytes + 16 * ((tid & 7) ^ swz(tid >> 3));
@@ -406,7 +432,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
             if (wave < TN / 64)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    gv[i] = f16_bits_to_f32(gsrc[min(b0 + i, nb - 1) / gsteps]);
+                    gv[i] = channel_scale(gsrc[min(b0 + i, nb - 1) / gsteps]);
     };
     // row r = 16 (FM u + j) + c of the tile: entry j of (u, c)
     const int fpos = ((tid / (16 * FM)) * 16 + (tid & 15)) * FM + (tid >> 4) % FM;
@@ -441,101 +467,140 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
     const int c0 = cg ^ swz(col), c1 = (cg + (TERN ? 2 : 4)) ^ swz(col);
     const int wa = TERN ? wn * FN * 32 + lane : (wn * FN * 16 + col) * 8;
 
-    auto compute = [&](auto S, int b) {
+    // Operands on their way from LDS: w's two fragments ahead (ternary: two
+    // fragments by one load), all of x's, and the scales.
+    u32x4_v rw[2][2], rx[FM][2];
+    fm_t fn, f, fp;          // the next step's, this step's, the last one's
+    // matrix results not yet scaled, and two fragments' channels' scales.  A
+    // result is scaled behind the second matrix instruction after its own: it is there by then.
+    constexpr int LAG = 2;
+    static_assert(FM >= LAG && FN * FM % 4 == 0);
+    f32x4_t d[4], gs[2];
+    auto read_w = [&](auto S, int i) {
         constexpr int s = decltype(S)::value;
-        // Raw operand of fragment i (ternary: of i and i + 1), read ahead.
-        struct Raw {
-            u32x4_v a, b;
-        };
-        auto read_w = [&](int i) -> Raw {
-            Raw r = {};
-            if constexpr (TERN) {
-                r.a = lw[s][wa + i * 32];
-            } else {
-                r.a = lw[s][wa + i * 128 + c0];
-                r.b = lw[s][wa + i * 128 + c1];
-            }
-            return r;
-        };
-        u32x2_v next_codes = {0, 0};
-        auto operand = [&](const Raw &r, int i) -> i32x8_v {
-            if constexpr (TERN) {
-                u32x2_v w = next_codes;
-                if (i % 2 == 0) {
-                    const u32x2_v lo = __builtin_amdgcn_permlane32_swap(r.a.x, r.a.z, false, false);
-                    const u32x2_v hi = __builtin_amdgcn_permlane32_swap(r.a.y, r.a.w, false, false);
-                    w = u32x2_v{lo.x, hi.x};
-                    next_codes = u32x2_v{lo.y, hi.y};
-                }
-                int d[4];
-                codes_to_fp4(w.x, d[0], d[1]);
-                codes_to_fp4(w.y, d[2], d[3]);
-                return i32x8_v{d[0], d[1], d[2], d[3], 0, 0, 0, 0};
-            } else {
-                return join(r.a, r.b);
-            }
-        };
-        i32x8_v xf[FM];
-        Raw raw = read_w(0);
-        const fm_t f = sf[TERN ? 0 : (wn * FN * 16) / 128][b & 7][wm * 16 + col];
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-            const u32x4_v a = lx[s][xa + j * 128 + c0], c = lx[s][xa + j * 128 + c1];
-            xf[j] = TERN ? odd_even(a, c) : join(a, c);
+        if constexpr (TERN) {
+            if (i % 2 == 0)
+                rw[0][0] = lw[s][wa + i * 32];
+        } else {
+            rw[i & 1][0] = lw[s][wa + i * 128 + c0];
+            rw[i & 1][1] = lw[s][wa + i * 128 + c1];
         }
-        // Each matrix instruction is followed by the scaling of a result of the
-        // fragment before, so that neither waits for the other.
-        f32x4_t d[2][FM], gs[2];
+    };
+    auto read_x = [&](auto S, int j) {
+        constexpr int s = decltype(S)::value;
+        rx[j][0] = lx[s][xa + j * 128 + c0];
+        rx[j][1] = lx[s][xa + j * 128 + c1];
+    };
+    auto read_f = [&](int b) { fn = sf[TERN ? 0 : (wn * FN * 16) / 128][b & 7][wm * 16 + col]; };
+    u32x2_v odd_codes = {0, 0};  // of the second fragment of two
+    auto w_operand = [&](int i) -> i32x8_v {
+        if constexpr (TERN) {
+            u32x2_v w = odd_codes;
+            if (i % 2 == 0) {
+                const u32x4_v r = rw[0][0];
+                const u32x2_v lo = __builtin_amdgcn_permlane32_swap(r.x, r.z, false, false);
+                const u32x2_v hi = __builtin_amdgcn_permlane32_swap(r.y, r.w, false, false);
+                w = u32x2_v{lo.x, hi.x};
+                odd_codes = u32x2_v{lo.y, hi.y};
+            }
+            int c[4];
+            codes_to_fp4(w.x, c[0], c[1]);
+            codes_to_fp4(w.y, c[2], c[3]);
+            return i32x8_v{c[0], c[1], c[2], c[3], 0, 0, 0, 0};
+        } else {
+            return join(rw[i & 1][0], rw[i & 1][1]);
+        }
+    };
+    auto scale_add = [&](int n, const fm_t &by) {  // result n of a step
+        const int i = n / FM, j = n % FM;
 #pragma unroll
-        for (int i = 0; i <= FN; ++i) {
-            const i32x8_v a = i < FN ? operand(raw, i) : i32x8_v{};
-            if (TERN ? i % 2 == 0 && i + 2 < FN : i + 1 < FN)
-                raw = read_w(TERN ? i + 2 : i + 1);
+        for (int k = 0; k < 4; ++k)
+            acc[i][j][k] += d[n & 3][k] * (G ? by[j] * gs[i & 1][k] : by[j]);
+    };
+
+    // Step b, from stage s.  Each matrix instruction is followed by the scaling of a
+    // result of the fragment before, so that neither waits for the other.  The
+    // waves meet two fragments before the end, once the stage is read and the next one is there:
+    // from then on this stage takes step b + 2, and the next step's first
+    // operands are read behind the last fragments' matrix instructions.
+    auto step = [&](auto S, int b) {
+        constexpr int s = decltype(S)::value;
+        constexpr std::integral_constant<int, s ^ 1> T;
+        static_assert(FN % 2 == 0 && FN >= 4);
+        i32x8_v x[FM];
+        fp = f;
+        f = fn;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const i32x8_v a = w_operand(i);
+            f32x4_t gnew;
             if constexpr (G)
-                if (i < FN)
-                    gs[i & 1] = sg[b & 7][(wn * FN + i) * 4 + g];
+                gnew = sg[b & 7][(wn * FN + i) * 4 + g];
+            if (i == FN - 2) {
+                meet();
+                issue(S, min(b + 2, nb - 1));
+                if constexpr (s == 0) {
+                    // scales ahead: loaded at the first step of four, put into LDS at the third
+                    if (b & 2)
+                        store_factors(b + 2);
+                    else
+                        load_factors(b + 4);
+                }
+                read_f(b + 1);
+            }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int j = 0; j < FM; ++j) {
-                if (i < FN)
-                    d[i & 1][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        a, xf[j], zero, TERN ? kFp4 : kFp8, kFp8, 0, TERN ? kHalf : kOne, 0, kOne);
-                if (i > 0)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[i > 0 ? i - 1 : 0][j][k] += d[(i & 1) ^ 1][j][k] * (G ? f[j] * gs[(i & 1) ^ 1][k] : f[j]);
+                const int n = i * FM + j;
+                if (i == 0)
+                    x[j] = TERN ? odd_even(rx[j][0], rx[j][1]) : join(rx[j][0], rx[j][1]);
+                asm volatile("" : "+v"(x[j]));  // (nothing: keeps the instruction from moving up)
+                d[n & 3] = mfma<TERN>(a, x[j]);
+                if (i == FN - 1)
+                    read_x(T, j);
+                if (G && j == LAG)
+                    gs[i & 1] = gnew;
+                const int m = n >= LAG ? n - LAG : n - LAG + FN * FM;
+                scale_add(m, n >= LAG ? f : fp);
+                asm volatile("" : "+v"(acc[m / FM][m % FM]));  // (the same, down)
                 __builtin_amdgcn_sched_barrier(0);
             }
+            if (i + 2 < FN)
+                read_w(S, i + 2);
+            else
+                read_w(T, i + 2 - FN);
         }
     };
 
     load_factors(0);
     store_factors(0);
+    // Every step loads the stage of the step after the next; the last ones load the
+    // last step again, into a stage that is not read (a branch there, or a second exit of the loop, had
+    // the compiler copy the step).
     issue(std::integral_constant<int, 0>(), 0);
-    // the factors of steps 0 .. 3 must be in LDS before the first barrier is passed
-    __builtin_amdgcn_s_waitcnt(0);
-    // Every step loads the next one's stage (the last loads itself again, into
-    // a stage that is not read: a branch there had the compiler copy the step, and
-    // so did a second exit of the loop).
+    issue(std::integral_constant<int, 1>(), min(1, nb - 1));
+    meet();
+    read_w(std::integral_constant<int, 0>(), 0);
+    read_w(std::integral_constant<int, 0>(), 1);
+    read_f(0);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+        read_x(std::integral_constant<int, 0>(), j);
+        f[j] = 0.f;
+    }
+    d[2] = d[3] = zero;
+    gs[1] = zero;
     int b = 0;
     for (; b + 1 < nb; b += 2) {
-        wait_and_barrier<0>();
-        issue(std::integral_constant<int, 1>(), b + 1);
-        // scales of the steps ahead: loaded at the first of four, put into LDS at the third
-        if (b & 2)
-            store_factors(b + 2);
-        else
-            load_factors(b + 4);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(std::integral_constant<int, 0>(), b);
-        wait_and_barrier<0>();
-        issue(std::integral_constant<int, 0>(), min(b + 2, nb - 1));
-        __builtin_amdgcn_sched_barrier(0);
-        compute(std::integral_constant<int, 1>(), b + 1);
+        step(std::integral_constant<int, 0>(), b);
+        step(std::integral_constant<int, 1>(), b + 1);
     }
-    wait_and_barrier<0>();
     if (b < nb)
-        compute(std::integral_constant<int, 0>(), b);
+        step(std::integral_constant<int, 0>(), b);
+#pragma unroll
+    for (int n = FN * FM - LAG; n < FN * FM; ++n)
+        scale_add(n, f);
+    meet();  // no load into LDS outlives the workgroup
 
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
@@ -544,7 +609,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
         if constexpr (TERN && !G)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-                cs[k] = f16_bits_to_f32(p.t_scale[(int64_t)e * p.N + min(ch + k, p.N - 1)]);
+                cs[k] = channel_scale(p.t_scale[(int64_t)e * p.N + min(ch + k, p.N - 1)]);
 #pragma unroll
         for (int j = 0; j < FM; ++j) {
             const int row = r0 + (wm * FM + j) * 16 + col;
@@ -557,7 +622,8 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
 template <bool TERN, class C>
 hipError_t launch_tiles(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 {
-    const int64_t wgs = tiles * ((p.N + C::TN - 1) / C::TN);
+    const int ntn = (p.N + C::TN - 1) / C::TN;
+    const int64_t wgs = TERN ? (tiles + 7) / 8 * 8 * ntn : (tiles * ntn + 7) / 8 * 8;
     if (wgs > INT32_MAX)
         return hipErrorInvalidValue;
     with_dtype(p.dtype, [&](auto dt) {
@@ -593,7 +659,7 @@ hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream)
         return launch_stream<true, 1>(p, expert_tiles(p, 16), stream);
     if (p.M <= 32 * p.E)
         return launch_stream<true, 4>(p, expert_tiles(p, 64), stream);
-    return launch_tiles<true, Tile<256, 256, 2, 4>>(p, expert_tiles(p, 256), stream);
+    return launch_tiles<true, Tile<256, 128, 4, 2>>(p, expert_tiles(p, 128), stream);
 }
 
 }  // namespace ternary
