@@ -32,45 +32,70 @@ __device__ __forceinline__ f32x4_t mfma(i32x8_v w, i32x8_v x)
 // Scale of a channel's fp4 products.
 __device__ __forceinline__ float channel_scale(uint16_t s) { return 0.5f * f16_bits_to_f32(s); }
 
+// Inclusive sum over the lanes of a wave (row shifts, then each row's total to
+// the rows after it).
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15, 31
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
+    return v;
+}
+
 // Places [r0, r1) of expert e that the idx-th tile of BM rows covers (tiles run
-// expert by expert); false past the last.  Every lane of a wave calls it.
+// expert by expert); false past the last.  Every lane of a wave calls it; lane l
+// looks at experts EP l .. EP l + EP - 1.  Whatever the offsets hold, the places are within
+// [0, R) and the expert within [0, E).
+template <int BM, int EP>
+__device__ __forceinline__ bool find_tile_of(const int32_t *offsets, int E, int R, int idx, int &e,
+                                             int &r0, int &r1)
+{
+    const int lo = (threadIdx.x & 63) * EP;
+    int o[EP + 1];
+#pragma unroll
+    for (int i = 0; i <= EP; ++i)
+        o[i] = offsets[min(lo + i, E)];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < EP; ++i) {
+        const int n = min(o[i + 1], R) - max(o[i], 0);
+        mine += n > 0 ? (n + BM - 1) / BM : 0;
+    }
+    const int incl = wave_scan(mine);
+    int left = idx - (incl - mine), fe = -1, f0 = 0, f1 = 0;
+    const uint64_t here = __builtin_amdgcn_ballot_w64(left >= 0 && left < mine);
+    if (!here)
+        return false;
+#pragma unroll
+    for (int i = 0; i < EP; ++i) {
+        const int a = max(o[i], 0), b = min(o[i + 1], R);
+        const int tiles = b > a ? (b - a + BM - 1) / BM : 0;
+        if (left >= 0 && left < tiles) {
+            fe = lo + i;
+            f0 = a + left * BM;
+            f1 = min(b, f0 + BM);
+        }
+        left -= tiles;
+    }
+    const int from = __builtin_ctzll(here);
+    e = __builtin_amdgcn_readlane(fe, from);
+    r0 = __builtin_amdgcn_readlane(f0, from);
+    r1 = __builtin_amdgcn_readlane(f1, from);
+    return e >= 0;
+}
+
 template <int BM>
 __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int R, int idx, int &e,
                                           int &r0, int &r1)
 {
-    const int lane = threadIdx.x & 63, per = (E + 63) / 64, lo = lane * per;
-    int mine = 0;
-    for (int i = 0; i < per; ++i)
-        if (lo + i < E) {
-            const int a = max(offsets[lo + i], 0), b = min(offsets[lo + i + 1], R);
-            mine += b > a ? (b - a + BM - 1) / BM : 0;
-        }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int u = __shfl_up(incl, o);
-        incl += lane >= o ? u : 0;
-    }
-    const uint64_t over = __builtin_amdgcn_ballot_w64(incl > idx);
-    if (!over)
-        return false;
-    const int from = __builtin_ctzll(over);
-    int left = idx - __shfl(incl - mine, from);
-    for (int i = 0; i < per; ++i) {
-        const int x = from * per + i;
-        if (x >= E)
-            break;
-        const int a = max(offsets[x], 0), b = min(offsets[x + 1], R);
-        const int tiles = b > a ? (b - a + BM - 1) / BM : 0;
-        if (left >= 0 && left < tiles) {
-            e = x;
-            r0 = a + left * BM;
-            r1 = min(b, r0 + BM);
-            return true;
-        }
-        left -= tiles;
-    }
-    return false;
+    if (E <= 64)
+        return find_tile_of<BM, 1>(offsets, E, R, idx, e, r0, r1);
+    if (E <= 256)
+        return find_tile_of<BM, 4>(offsets, E, R, idx, e, r0, r1);
+    return find_tile_of<BM, 8>(offsets, E, R, idx, e, r0, r1);
 }
 
 // 16 codes (one word) -> the fp4 words of its odd and of its even codes (the
@@ -118,118 +143,16 @@ __device__ __forceinline__ void put4(const Fp8Product &p, int row, int ch, f32x4
     }
 }
 
-constexpr int kWaves = 4, kThreads = kWaves * 64;
-
-// A workgroup computes 16 channels x 16 MT rows; its waves share the K blocks
-// out and meet in LDS.  Operands go straight from memory to registers.
-template <bool TERN, int MT, int DT>
-__global__ void __launch_bounds__(kThreads) stream_kernel(const Fp8Product p)
+// The same for y's type as the argument gives it.
+__device__ __forceinline__ void put4(const Fp8Product &p, int row, int ch, f32x4_t s)
 {
-    __shared__ f32x4_t red[kWaves][MT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, col = lane & 15;
-    const int n0 = blockIdx.x * 16, nb = p.nb;
-    int e = 0, r0 = blockIdx.y * 16 * MT, r1 = min(p.M, r0 + 16 * MT);
-    if constexpr (TERN)
-        if (!find_tile<16 * MT>(p.offsets, p.E, p.M, blockIdx.y, e, r0, r1))
-            return;
-
-    // this lane's row of x in each fragment (rows past the last repeat it; their
-    // results are not stored)
-    const uint8_t *xp[MT];
-    const float *sp[MT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j) {
-        int64_t row = min(r0 + 16 * j + col, r1 - 1);
-        if constexpr (TERN)
-            if (p.order)
-                row = p.order[row] / p.top_k;
-        if constexpr (TERN)
-            row = row < 0 || row >= p.x_rows ? 0 : row;
-        xp[j] = p.x + row * nb * kFp8Block;
-        sp[j] = p.x_scale + row * nb;
-    }
-    const int n = min(n0 + col, p.N - 1);  // this lane's channel of A
-    const uint8_t *wp;
-    if constexpr (TERN)
-        wp = p.w + ((int64_t)e * ((p.N + 15) / 16) + blockIdx.x) * ((nb + 1) / 2) * kTileBytes;
+    if (p.dtype == TERNARY_BF16)
+        put4<TERNARY_BF16>(p, row, ch, s);
+    else if (p.dtype == TERNARY_FP16)
+        put4<TERNARY_FP16>(p, row, ch, s);
     else
-        wp = p.w + (int64_t)n * nb * kFp8Block;
-
-    f32x4_t acc[MT];
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-        acc[j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-    for (int b = wave; b < nb; b += kWaves) {
-        i32x8_v a;
-        float ws[4] = {1.f, 1.f, 1.f, 1.f};
-        if constexpr (TERN) {
-            // lane group g: codes 32 g .. 32 g + 31 of the block
-            const u32x2_v w = *reinterpret_cast<const u32x2_v *>(
-                wp + (b >> 1) * kTileBytes + ((b & 1) * 2 + (g >> 1)) * 256 + col * 16 + (g & 1) * 8);
-            int f[4];
-            codes_to_fp4(w.x, f[0], f[1]);
-            codes_to_fp4(w.y, f[2], f[3]);
-            a = i32x8_v{f[0], f[1], f[2], f[3], 0, 0, 0, 0};
-            if (p.group) {
-                const int gi = (int)((int64_t)b * kFp8Block / p.group);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    ws[i] = channel_scale(
-                        p.t_scale[((int64_t)e * p.N + min(n0 + 4 * g + i, p.N - 1)) * p.ngroups + gi]);
-            }
-        } else {
-            const u32x4_v *w = reinterpret_cast<const u32x4_v *>(wp + b * kFp8Block + 16 * g);
-            a = join(w[0], w[4]);
-            ws[0] = p.w_scale[(int64_t)(n0 / kFp8Block) * nb + b];
-        }
-#pragma unroll
-        for (int j = 0; j < MT; ++j) {
-            const u32x4_v *xv = reinterpret_cast<const u32x4_v *>(xp[j] + b * kFp8Block + 16 * g);
-            const float xs = sp[j][b];
-            f32x4_t d;
-            if constexpr (TERN)
-                d = mfma<true>(a, odd_even(xv[0], xv[4]));
-            else
-                d = mfma<false>(a, join(xv[0], xv[4]));
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                acc[j][i] += d[i] * (TERN ? xs * ws[i] : xs * ws[0]);
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < MT; ++j)
-        red[wave][j][lane] = acc[j];
-    __syncthreads();
-    // the waves' sums, in their order
-    for (int j = wave; j < MT; j += kWaves) {
-        f32x4_t s = red[0][j][lane];
-        for (int w = 1; w < kWaves; ++w)
-            s += red[w][j][lane];
-        const int row = r0 + 16 * j + col, ch = n0 + 4 * g;
-        if (row >= r1)
-            continue;
-        if constexpr (TERN)
-            if (!p.group)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    s[i] *= channel_scale(p.t_scale[(int64_t)e * p.N + min(ch + i, p.N - 1)]);
-        put4<DT>(p, row, ch, s);
-    }
+        put4<TERNARY_FP32>(p, row, ch, s);
 }
-
-template <bool TERN, int MT>
-hipError_t launch_stream(const Fp8Product &p, int64_t tiles, hipStream_t stream)
-{
-    const unsigned nx = (unsigned)((p.N + 15) / 16);
-    with_dtype(p.dtype, [&](auto dt) {
-        hipLaunchKernelGGL((stream_kernel<TERN, MT, decltype(dt)::value>), dim3(nx, (unsigned)tiles),
-                           dim3(kThreads), 0, stream, p);
-    });
-    return hipGetLastError();
-}
-
-// ---------------------------------------------------------------- many rows
 
 // Waits for everything this wave has loaded (LDS reads, and loads into LDS among
 // them), then for the workgroup's other waves.
@@ -272,6 +195,309 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t make_rsrc(const void *base, ui
 // c ^ swz(r), which spreads the rows that a fragment read touches over the banks.
 __device__ __forceinline__ int swz(int r) { return r & 7; }
 
+// ---------------------------------------------------------------- few rows
+//
+// Weights are read once, so the kernel is a stream of them: they go straight
+// from memory to registers, a chunk of U blocks at a time with all its loads
+// issued together, and the eight waves of a workgroup share K out (`ks` ways; the others
+// take further channels) and meet once, in LDS.  A wave holds 16 FN channels x
+// 16 MT rows.  x is read again (from L2) for every 16 FN channels; it passes
+// through LDS, each wave's own part, because the operand's lane order (16 rows
+// in neighbouring lanes) would cost a cache access per lane: at 45 rows of 18944 x 4096
+// the accesses of L1, not HBM, bounded a kernel that loaded x like w (39 us).
+
+constexpr int kWaves = 8, kThreads = kWaves * 64;
+// Blocks of a chunk: as many as leave room for two workgroups' x in a compute unit's LDS.
+constexpr int thin_chunk(int mt) { return mt == 1 ? 4 : mt == 2 ? 2 : 1; }
+
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x2_u __attribute__((ext_vector_type(2), aligned(4)));
+// weights' scales are read by scalar loads: the same for a whole wave
+typedef const __attribute__((address_space(4))) float constant_float;
+
+// Values b0 .. b0 + U - 1 of a row of n; past its end 0.
+template <int U>
+__device__ __forceinline__ void load_scales(const float *row, int b0, int n, float v[U])
+{
+    static_assert(U == 1 || U == 2 || U == 4);
+    if (n < U || b0 + U > n) {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            v[i] = row[min(b0 + i, n - 1)];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            v[i] = b0 + i < n ? v[i] : 0.f;
+    } else if constexpr (U == 4) {
+        const f32x4_u u = *reinterpret_cast<const f32x4_u *>(row + b0);
+        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+    } else if constexpr (U == 2) {
+        const f32x2_u u = *reinterpret_cast<const f32x2_u *>(row + b0);
+        v[0] = u.x, v[1] = u.y;
+    } else {
+        v[0] = row[b0];
+    }
+}
+
+typedef uint16_t u16x4_u __attribute__((ext_vector_type(4), aligned(2)));
+
+// Group scales (fp16) of blocks b0 .. b0 + U - 1 of a channel of n groups of `gb`
+// blocks; past its end the last.
+template <int U>
+__device__ __forceinline__ void load_group_scales(const uint16_t *row, int b0, int gb, int n, uint16_t v[U])
+{
+    if (U == 4 && gb == 1 && b0 + U <= n) {
+        const u16x4_u u = *reinterpret_cast<const u16x4_u *>(row + b0);
+        v[0] = u.x, v[1] = u.y, v[2 % U] = u.z, v[3 % U] = u.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            v[i] = row[min((b0 + i) / gb, n - 1)];
+    }
+}
+
+// TERN: ternary weights of experts (G: with group scales).
+template <bool TERN, bool G, int MT, int FN>
+__global__ void __launch_bounds__(kThreads, 4) thin_kernel(const Fp8Product p, int ks)
+{
+    constexpr int U = thin_chunk(MT);
+    typedef float u_t __attribute__((ext_vector_type(U)));  // scales of a chunk
+    // x's chunks, then (once they are done with) the waves' sums
+    constexpr int XU4 = U * MT * 128, RU4 = FN * MT * 64;
+    __shared__ __attribute__((aligned(16))) u32x4_v sx[kWaves * (XU4 > RU4 ? XU4 : RU4)];
+    __shared__ __attribute__((aligned(16))) u_t ss[kWaves][MT][16];
+    __shared__ __attribute__((aligned(16))) uint16_t sg[kWaves][G ? U : 1][G ? FN * 16 : 4];
+    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nb = p.nb, kpart = wave % ks, parts = kWaves / ks;
+    // workgroups run over the channels first: those of one tile of rows are neighbours
+    const int ntn = (p.N + 16 * FN * parts - 1) / (16 * FN * parts);
+    const int tm = blockIdx.x / ntn, n0 = ((blockIdx.x - tm * ntn) * parts + wave / ks) * 16 * FN;
+    int e = 0, r0 = tm * 16 * MT, r1 = min(p.M, r0 + 16 * MT);
+    if constexpr (TERN)
+        if (!find_tile<16 * MT>(p.offsets, p.E, p.M, tm, e, r0, r1))
+            return;
+
+    // This lane's weights: of channel col of each fragment, chunks like x's, or
+    // a ternary slab's 16 bytes at 16 * lane.  (Channels past N repeat the last.)
+    const u32x4_v *wp[FN];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+        if constexpr (TERN) {
+            const int blocks = (p.N + 15) / 16, blk = min(n0 / 16 + i, blocks - 1);
+            wp[i] = reinterpret_cast<const u32x4_v *>(
+                        p.w + ((int64_t)e * blocks + blk) * ((nb + 1) / 2) * kTileBytes) + lane;
+        } else {
+            wp[i] = reinterpret_cast<const u32x4_v *>(p.w + (int64_t)min(n0 + 16 * i + col, p.N - 1) * nb * kFp8Block) + g;
+        }
+    }
+    constexpr int WL = TERN ? U / 2 : 2 * U;  // weight loads of a fragment and chunk
+    u32x4_v w[FN][WL];
+    auto load_w = [&](int b0) {  // (blocks past the last: the last again)
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int u = 0; u < WL; ++u) {
+                if constexpr (TERN)
+                    w[i][u] = wp[i][min(b0 / 2 + u, (nb - 1) / 2) * 64];
+                else
+                    w[i][u] = wp[i][min(b0 + u / 2, nb - 1) * 8 + 4 * (u & 1)];
+            }
+    };
+    load_w(kpart * U);  // on their way while the rows of x are looked up
+
+    // Rows of x.  Lane l loads chunk (l % 8) ^ (l / 8) of row l / 8 of eight rows
+    // at a time (the swizzle of the stages below); rows past the last repeat it.
+    auto x_row = [&](int r) -> int64_t {
+        int64_t row = min(r0 + r, r1 - 1);
+        if constexpr (TERN) {
+            if (p.order)
+                row = p.order[row] / p.top_k;
+            row = row < 0 || row >= p.x_rows ? 0 : row;
+        }
+        return row;
+    };
+    const int rows = r1 - r0;
+    const uint8_t *xp[2 * MT];
+#pragma unroll
+    for (int q = 0; q < 2 * MT; ++q)
+        xp[q] = p.x + x_row(8 * q + (lane >> 3)) * nb * kFp8Block + 16 * ((lane & 7) ^ (lane >> 3));
+    // Their scales: lanes 0 .. 15 load a fragment's, for all.
+    const float *sp[MT];
+#pragma unroll
+    for (int j = 0; j < MT; ++j)
+        sp[j] = p.x_scale + x_row(16 * j + col) * nb;
+    // Chunks of a row that lane group g holds: g and g + 4, or for ternary
+    // weights (see below) those of 0, 1, 4, 5 and two further on.
+    const int cg = TERN ? g + (g & 2) : g;
+    const int c0 = cg ^ (col & 7), c1 = (cg + (TERN ? 2 : 4)) ^ (col & 7);
+    lds_u4 *const lx = (lds_u4 *)sx + wave * (U * MT * 128);
+    const int xa = (col >> 3) * 64 + (col & 7) * 8;
+    constant_float *wsp = TERN ? nullptr : (constant_float *)(p.w_scale + (int64_t)min(n0 / kFp8Block, (p.N - 1) / kFp8Block) * nb);
+    static_assert(FN <= 4, "a wave's channels share w's scales");
+
+    f32x4_t acc[FN][MT];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    // Blocks past the last load that again, and count with scale 0.
+    for (int b0 = kpart * U; b0 < nb; b0 += ks * U) {
+        float ws[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int q = 0; q < 2 * MT; ++q)
+                if (8 * q < rows)
+                    load_to_lds(xp[q] + min(b0 + u, nb - 1) * kFp8Block, lx + (u * 2 * MT + q) * 64);
+        if (lane < 16) {
+            float v[MT][U];
+#pragma unroll
+            for (int j = 0; j < MT; ++j)
+                load_scales<U>(sp[j], b0, nb, v[j]);
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                u_t t;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    t[u] = v[j][u];
+                ss[wave][j][lane] = t;
+            }
+        }
+        if constexpr (!TERN)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                ws[u] = wsp[min(b0 + u, nb - 1)];
+        if constexpr (G)
+            if (lane < 16 * FN) {  // a channel a lane
+                uint16_t v[U];
+                load_group_scales<U>(p.t_scale + ((int64_t)e * p.N + min(n0 + lane, p.N - 1)) * p.ngroups, b0,
+                                     p.group / kFp8Block, p.ngroups, v);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    sg[wave][u][lane] = v[u];
+            }
+        // x is there once this wave's loads are done: no other wave reads it
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(7 << 4);
+        __builtin_amdgcn_wave_barrier();
+        u_t xs[MT];
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            xs[j] = ss[wave][j][col];
+        i32x8_v a[FN][2];
+        f32x4_t gs[FN];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                if constexpr (TERN) {
+                    // A slab holds codes 64 q .. 64 q + 63 in lanes 16 q up; exchanging the
+                    // halves of a wave (permlane32_swap) leaves a block's codes 0, 64, 32 and 96 (and
+                    // 31 more) in its four lane groups.
+                    if (u % 2 == 0) {
+                        const u32x4_v r = w[i][u / 2];
+                        const u32x2_v lo = __builtin_amdgcn_permlane32_swap(r.x, r.z, false, false);
+                        const u32x2_v hi = __builtin_amdgcn_permlane32_swap(r.y, r.w, false, false);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            int c[4];
+                            codes_to_fp4(h ? lo.y : lo.x, c[0], c[1]);
+                            codes_to_fp4(h ? hi.y : hi.x, c[2], c[3]);
+                            a[i][h] = i32x8_v{c[0], c[1], c[2], c[3], 0, 0, 0, 0};
+                        }
+                    }
+                } else {
+                    a[i][u & 1] = join(w[i][2 * u], w[i][2 * u + 1]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < (G ? FN : 0); ++i) {
+                const u32x2_v q = *reinterpret_cast<const u32x2_v *>(&sg[wave][G ? u : 0][16 * i + 4 * g]);
+                gs[i] = f32x4_t{channel_scale((uint16_t)q.x), channel_scale((uint16_t)(q.x >> 16)),
+                                channel_scale((uint16_t)q.y), channel_scale((uint16_t)(q.y >> 16))};
+            }
+#pragma unroll
+            for (int j = 0; j < MT; ++j) {
+                const u32x4_v x0 = lx[(u * MT + j) * 128 + xa + c0], x1 = lx[(u * MT + j) * 128 + xa + c1];
+                const i32x8_v xv = TERN ? odd_even(x0, x1) : join(x0, x1);
+                const float f = TERN ? xs[j][u] : xs[j][u] * ws[u];
+#pragma unroll
+                for (int i = 0; i < FN; ++i) {
+                    const f32x4_t d = mfma<TERN>(a[i][u & 1], xv);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        acc[i][j][k] += d[k] * (G ? f * gs[i][k] : f);
+                }
+            }
+        }
+        // (the next chunk's x goes where this one's has been read)
+        __builtin_amdgcn_sched_barrier(0);
+        if (b0 + ks * U < nb)
+            load_w(b0 + ks * U);
+    }
+    __syncthreads();
+    f32x4_t(*const red)[FN * MT][64] = reinterpret_cast<f32x4_t(*)[FN * MT][64]>(sx);
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+            red[wave][i * MT + j][lane] = acc[i][j];
+    __syncthreads();
+    // the waves' sums, in their order: fragment q of wave group q / (FN MT)
+    for (int q = wave; q < parts * FN * MT; q += kWaves) {
+        const int w0 = q / (FN * MT) * ks, fr = q % (FN * MT), i = fr / MT, j = fr % MT;
+        f32x4_t s = red[w0][fr][lane];
+        for (int w = 1; w < ks; ++w)
+            s += red[w0 + w][fr][lane];
+        const int row = r0 + 16 * j + col;
+        const int ch = ((blockIdx.x - tm * ntn) * parts + q / (FN * MT)) * 16 * FN + 16 * i + 4 * g;
+        if (row >= r1)
+            continue;
+        if constexpr (TERN && !G)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                s[k] *= channel_scale(p.t_scale[(int64_t)e * p.N + min(ch + k, p.N - 1)]);
+        put4(p, row, ch, s);
+    }
+}
+
+// ks: ways to share K.  Each wave should have a chunk of its own, and the more
+// channels a workgroup holds the fewer there are, so no more ways than chunks.
+template <bool TERN, bool G, int MT, int FN>
+hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
+{
+    constexpr int U = thin_chunk(MT);
+    const int chunks = (p.nb + U - 1) / U;
+    const int ks = chunks >= 8 ? 8 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
+    const int64_t wgs = tiles * ((p.N + 16 * FN * (kWaves / ks) - 1) / (16 * FN * (kWaves / ks)));
+    if (wgs > INT32_MAX)
+        return hipErrorInvalidValue;
+    hipLaunchKernelGGL((thin_kernel<TERN, G, MT, FN>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, p, ks);
+    return hipGetLastError();
+}
+
+// One fragment of channels a wave where two would leave compute units without a workgroup.
+template <bool TERN, bool G, int MT>
+hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
+{
+    return (p.N + 15) / 16 * tiles < 1024 ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
+                                          : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
+}
+
+// Rows in tiles of 16 MT.
+template <bool TERN, int MT>
+hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
+{
+    if constexpr (TERN)
+        return p.group ? launch_thin<true, true, MT>(p, tiles, stream) : launch_thin<true, false, MT>(p, tiles, stream);
+    else
+        return launch_thin<false, false, MT>(p, tiles, stream);
+}
+
+// ---------------------------------------------------------------- many rows
+
 template <int TN_, int TM_, int WN_, int WM_>
 struct Tile {
     static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_;
@@ -279,28 +505,7 @@ struct Tile {
     static constexpr int FN = TN / WN / 16, FM = TM / WM / 16;  // fragments of a wave
 };
 
-// weights' scales are read by scalar loads: the same for a whole workgroup
-typedef const __attribute__((address_space(4))) float constant_float;
-typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
-
-// Values b0 .. b0 + 3 of a row of n (unspecified past its end).
-__device__ __forceinline__ f32x4_t load_scales(const float *row, int b0, int n)
-{
-    if (n < 4) {
-        return f32x4_t{row[min(b0, n - 1)], row[min(b0 + 1, n - 1)], row[min(b0 + 2, n - 1)], row[n - 1]};
-    }
-    // the row's last four at its end, moved down
-    const int at = min(b0, n - 4);
-    f32x4_u u = *reinterpret_cast<const f32x4_u *>(row + at);
-    if (at + 1 <= b0)
-        u = u.yzww;
-    if (at + 2 <= b0)
-        u = u.yzww;
-    if (at + 3 <= b0)
-        u = u.yzww;
-    return f32x4_t{u.x, u.y, u.z, u.w};
-}
-// The same for a row that a whole workgroup reads (scalar loads).
+// Values b0 .. b0 + 3 of a row of n (past its end the last) that a whole workgroup reads.
 __device__ __forceinline__ f32x4_t load_scales_uniform(const float *row, int b0, int n)
 {
     constant_float *r = (constant_float *)row;
@@ -422,8 +627,11 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
     };
     f32x4_t fx = {0.f, 0.f, 0.f, 0.f}, fw[QB], gv = fx;
     auto load_factors = [&](int b0) {  // of steps b0 .. b0 + 3
-        if (wave < TM / 64)
-            fx = load_scales(fsrc, b0, nb);
+        if (wave < TM / 64 && b0 < nb) {
+            float v[4];
+            load_scales<4>(fsrc, b0, nb, v);
+            fx = f32x4_t{v[0], v[1], v[2], v[3]};
+        }
         if constexpr (!TERN)
 #pragma unroll
             for (int q = 0; q < QB; ++q)
@@ -647,18 +855,22 @@ int64_t expert_tiles(const Fp8Product &p, int rows)
 hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
 {
     if (p.M <= 16)
-        return launch_stream<false, 1>(p, 1, stream);
+        return launch_thin<false, 1>(p, 1, stream);
+    if (p.M <= 32)
+        return launch_thin<false, 2>(p, 1, stream);
+    if (p.M <= 48)
+        return launch_thin<false, 3>(p, 1, stream);
     if (p.M < 256)
-        return launch_stream<false, 4>(p, (p.M + 63) / 64, stream);
+        return launch_thin<false, 4>(p, (p.M + 63) / 64, stream);
     return launch_tiles<false, Tile<256, 256, 2, 4>>(p, (p.M + 255) / 256, stream);
 }
 
 hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream)
 {
     if (p.M <= 16 * p.E)
-        return launch_stream<true, 1>(p, expert_tiles(p, 16), stream);
+        return launch_thin<true, 1>(p, expert_tiles(p, 16), stream);
     if (p.M <= 32 * p.E)
-        return launch_stream<true, 4>(p, expert_tiles(p, 64), stream);
+        return launch_thin<true, 2>(p, expert_tiles(p, 32), stream);
     return launch_tiles<true, Tile<256, 128, 4, 2>>(p, expert_tiles(p, 128), stream);
 }
 

@@ -1,7 +1,7 @@
 // Routing tokens to experts on gfx950: scores, top-k, weights, and the token
 // slots sorted by expert.
 //
-// A wave takes a token; lane l holds experts l, l + 64, ...  Scores, group
+// A wave takes a token; a lane holds one to eight neighbouring experts.  Scores, group
 // worths and weights are 64-bit: among the thousands of choices of a batch some
 // are between experts whose scores agree to 1e-7, which 32 bits would decide by
 // their rounding; E exponentials a token in 64 bits cost little beside the
@@ -15,7 +15,7 @@
 // workgroup routes and sorts (one launch); more are routed by a workgroup per
 // 16 tokens, whose masks go to the workspace, and placed by a second kernel, a
 // workgroup per 64 tokens, each adding up the masks of all chunks itself
-// (2 bytes per chunk and expert, from L2).  Beyond kFlatTokens that sum would
+// (2 bytes per chunk and expert, from L2, 16 bytes a load).  Beyond kFlatTokens that sum would
 // grow with the square of the batch, so a kernel in between adds it up per
 // 1024 tokens.
 #include <cfloat>
@@ -35,113 +35,191 @@ constexpr int kSuper = 1024;        // tokens of a row of sums
 constexpr int kFlatTokens = 8192;   // most tokens without the rows of sums
 constexpr int kMaxE = TERNARY_MAX_EXPERTS, kMaxK = TERNARY_MAX_TOP_K;
 
-__device__ __forceinline__ double shfl_xor_d(double v, int o) { return __shfl_xor(v, o); }
+// v of another lane by a data-parallel move (0 where there is none): CTRL
+// 0x111, 0x112, 0x114, 0x118 one to eight lanes up a row of 16, 0x142 and 0x143 the last lane of a row
+// and of two rows to those after it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint64_t m = (uint64_t)moved<CTRL, ROWS>((uint32_t)(b >> 32)) << 32 | moved<CTRL, ROWS>((uint32_t)b);
+    return __builtin_bit_cast(double, m);
+}
+
+// f over a wave, in lane 63, where 0 changes nothing.
+template <class T, class F>
+__device__ __forceinline__ T wave_fold(T v, F f)
+{
+    v = f(v, moved<0x111, 0xf>(v));
+    v = f(v, moved<0x112, 0xf>(v));
+    v = f(v, moved<0x114, 0xf>(v));
+    v = f(v, moved<0x118, 0xf>(v));
+    v = f(v, moved<0x142, 0xa>(v));
+    v = f(v, moved<0x143, 0xc>(v));
+    return v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v)
+{
+    v = wave_fold(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ double lane_value(double v, int lane)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)b, lane);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum(double v)
+{
+    return lane_value(wave_fold(v, [](double a, double b) { return a + b; }), 63);
+}
+// Unsigned numbers in the order of the floating ones (never 0 for a number or -inf).
+__device__ __forceinline__ uint32_t ordered(float v)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, v);
+    return b >> 31 ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ uint64_t ordered(double v)
+{
+    const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // (-0 is 0)
+    return b >> 63 ? ~b : b | 0x8000000000000000ull;
+}
 
 // The choices of one token (a wave): lane j < k gets its j-th expert and weight.
-// `group_lds`: E doubles of this wave's (used where groups > 1).
+// Lane l holds experts EP l .. EP l + EP - 1.  `group_lds`: E doubles of this wave's
+// (used where groups > 1).
 template <int DT, int EP>
 __device__ __forceinline__ void choose(const RouteArgs &a, int t, double *group_lds, int &my_id,
                                        float &my_w)
 {
-    const int lane = threadIdx.x & 63, E = a.E;
-    double p[EP], c[EP];
-    double mx = -INFINITY;
+    const int lane = threadIdx.x & 63, E = a.E, e0 = lane * EP;
+    float l[EP], bias[EP];
 #pragma unroll
     for (int i = 0; i < EP; ++i) {
-        const int e = i * 64 + lane;
-        float l = -INFINITY, b = 0.f;
-        if (e < E) {
-            l = load_elem<DT>(a.logits, (int64_t)t * E + e);
+        l[i] = -INFINITY, bias[i] = 0.f;
+        if (e0 + i < E) {
+            l[i] = load_elem<DT>(a.logits, (int64_t)t * E + e0 + i);
             if (a.bias)
-                b = a.bias[e];
+                bias[i] = a.bias[e0 + i];
         }
-        const bool open = l > -INFINITY && b > -INFINITY;  // NaN: false
-        p[i] = open ? (double)fminf(l, FLT_MAX) : -INFINITY;
-        c[i] = b;
-        mx = fmax(mx, p[i]);
     }
+    bool open[EP];
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EP; ++i) {
+        open[i] = l[i] > -INFINITY && bias[i] > -INFINITY;  // NaN: false
+        l[i] = open[i] ? fminf(l[i], FLT_MAX) : -INFINITY;
+        mx = fmaxf(mx, l[i]);
+    }
+    double p[EP];  // probabilities (softmax: times z)
+    double z = 1.0;
     if (a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < EP; ++i) {
-            const bool open = p[i] > -INFINITY;
-            p[i] = open ? 1.0 / (1.0 + exp(-p[i])) : 0.0;
-            c[i] = open ? p[i] + c[i] : -INFINITY;
-        }
+        for (int i = 0; i < EP; ++i)
+            p[i] = open[i] ? 1.0 / (1.0 + exp(-(double)l[i])) : 0.0;
     } else {
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1)
-            mx = fmax(mx, shfl_xor_d(mx, o));
-        double z = 0.0;
-        bool open[EP];
+        const uint32_t m = wave_max(ordered(mx));
+        mx = __builtin_bit_cast(float, m >> 31 ? m & 0x7fffffffu : ~m);
+        double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < EP; ++i) {
-            open[i] = p[i] > -INFINITY;
-            p[i] = open[i] ? exp(p[i] - mx) : 0.0;
-            z += p[i];
+            p[i] = open[i] ? exp((double)l[i] - (double)mx) : 0.0;
+            sum += p[i];
         }
+        z = wave_sum(sum);
 #pragma unroll
-        for (int o = 32; o >= 1; o >>= 1)
-            z += shfl_xor_d(z, o);
-#pragma unroll
-        for (int i = 0; i < EP; ++i) {
+        for (int i = 0; i < EP; ++i)
             p[i] = open[i] ? p[i] / z : 0.0;
-            c[i] = open[i] ? p[i] + c[i] : -INFINITY;
-        }
     }
+    double c[EP];
+#pragma unroll
+    for (int i = 0; i < EP; ++i)
+        c[i] = open[i] ? p[i] + (double)bias[i] : -INFINITY;
 
     if (a.groups > 1) {
-        // lane g < groups: its group's two largest, then the group's rank among all
-        const int per = E / a.groups;
-#pragma unroll
-        for (int i = 0; i < EP; ++i)
-            if (i * 64 + lane < E)
-                group_lds[i * 64 + lane] = c[i];
-        __builtin_amdgcn_wave_barrier();
+        // A group's worth, from its two largest.  Groups of whole lanes, a power of
+        // two of them, meet by exchanges; others through LDS, a lane a group.
+        const int per = E / a.groups, lanes = per / EP;
         double b1 = -INFINITY, b2 = -INFINITY;
-        if (lane < a.groups)
-            for (int i = 0; i < per; ++i) {
-                const double v = group_lds[lane * per + i];
-                b2 = fmax(b2, fmin(b1, v));
-                b1 = fmax(b1, v);
+        auto add = [&](double v) {
+            b2 = fmax(b2, fmin(b1, v));
+            b1 = fmax(b1, v);
+        };
+        const bool whole = per % EP == 0 && (lanes & (lanes - 1)) == 0;
+        if (whole) {
+#pragma unroll
+            for (int i = 0; i < EP; ++i)
+                add(c[i]);
+            for (int o = 1; o < lanes; o <<= 1) {
+                const double o1 = __shfl_xor(b1, o), o2 = __shfl_xor(b2, o);
+                add(o1);
+                b2 = fmax(b2, o2);  // o2 <= o1, which is in: it can only be second
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EP; ++i)
+                if (e0 + i < E)
+                    group_lds[e0 + i] = c[i];
+            __builtin_amdgcn_wave_barrier();
+            if (lane < a.groups)
+                for (int i = 0; i < per; ++i)
+                    add(group_lds[lane * per + i]);
+        }
         const double worth = b2 > -INFINITY ? b1 + b2 : b1;
+        const int mine = whole ? lane / lanes : lane;
         int rank = 0;
         for (int g = 0; g < a.groups; ++g) {
-            const double w = __shfl(worth, g);
-            rank += w > worth || (w == worth && g < lane) ? 1 : 0;
+            const double w = lane_value(worth, whole ? g * lanes : g);
+            rank += w > worth || (w == worth && g < mine) ? 1 : 0;
         }
-        const uint64_t kept = __builtin_amdgcn_ballot_w64(lane < a.groups && rank < a.top_groups);
+        const uint64_t kept = __builtin_amdgcn_ballot_w64(mine < a.groups && rank < a.top_groups);
 #pragma unroll
-        for (int i = 0; i < EP; ++i)
-            if (!(kept >> ((i * 64 + lane) / per) & 1))
-                c[i] = -INFINITY;
-        __builtin_amdgcn_wave_barrier();
+        for (int i = 0; i < EP; ++i) {
+            const bool keep = whole ? rank < a.top_groups : (kept >> min((e0 + i) / per, 63) & 1) != 0;
+            c[i] = keep ? c[i] : -INFINITY;
+        }
     }
 
+    // k rounds of the largest: by the high halves of the ordered scores, and only
+    // where two lanes agree in those by the low halves and the index.
+    uint64_t key[EP];
+#pragma unroll
+    for (int i = 0; i < EP; ++i)
+        key[i] = c[i] > -INFINITY ? ordered(c[i]) : 0;
     my_id = -1;
     double mine = 0.0, sum = 0.0;
     for (int j = 0; j < a.k; ++j) {
-        double best = c[0];
-        int id = lane;
+        uint64_t best = key[0];
+        int at = 0;
 #pragma unroll
         for (int i = 1; i < EP; ++i)
-            if (c[i] > best)
-                best = c[i], id = i * 64 + lane;
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) {
-            const double ob = shfl_xor_d(best, o);
-            const int oid = __shfl_xor(id, o);
-            if (ob > best || (ob == best && oid < id))
-                best = ob, id = oid;
+            if (key[i] > best)
+                best = key[i], at = i;
+        const uint32_t hi = wave_max((uint32_t)(best >> 32));
+        if (hi == 0)
+            break;  // none left (the same in every lane)
+        uint64_t with = __builtin_amdgcn_ballot_w64((uint32_t)(best >> 32) == hi);
+        if (with & (with - 1)) {
+            const uint32_t lo = (uint32_t)(best >> 32) == hi ? (uint32_t)best : 0;
+            const uint32_t most = wave_max(lo);
+            with = __builtin_amdgcn_ballot_w64((uint32_t)(best >> 32) == hi && (uint32_t)best == most);
         }
-        if (best == -INFINITY)
-            break;  // the same in every lane
+        const int from = __builtin_ctzll(with);  // the lowest lane holds the lowest index
         double w = 0.0;
 #pragma unroll
         for (int i = 0; i < EP; ++i)
-            if (i * 64 + lane == id)
-                w = p[i], c[i] = -INFINITY;
-        w = __shfl(w, id & 63);
+            if (at == i) {
+                w = p[i];
+                key[i] = lane == from ? 0 : key[i];
+            }
+        const int id = __builtin_amdgcn_readlane(e0 + at, from);
+        w = lane_value(w, from);
         sum += w;
         if (lane == j)
             my_id = id, mine = w;
@@ -223,7 +301,12 @@ __global__ void __launch_bounds__(kThreads) route_few_kernel(const RouteArgs a)
     }
 }
 
-// Many tokens: a wave each, and the masks of every 16 tokens, [T/16][E].
+__host__ __device__ inline int64_t chunks_of(int64_t T) { return (T + kChunk - 1) / kChunk; }
+// Masks lie in rows of whole 16 bytes; the rows of sums follow them.
+__host__ __device__ inline int mask_row(int64_t E) { return (int)((E + 7) & ~(int64_t)7); }
+__host__ __device__ inline int64_t mask_bytes(int64_t T, int64_t E) { return chunks_of(T) * mask_row(E) * 2; }
+
+// Many tokens: a wave each, and the masks of every 16 tokens, [T/16][mask_row(E)].
 template <int DT, int EP>
 __global__ void __launch_bounds__(kThreads) route_many_kernel(const RouteArgs a)
 {
@@ -246,16 +329,10 @@ __global__ void __launch_bounds__(kThreads) route_many_kernel(const RouteArgs a)
         }
     }
     __syncthreads();
-    uint16_t *out = static_cast<uint16_t *>(a.workspace) + (int64_t)blockIdx.x * a.E;
-    for (int e = tid; e < a.E; e += kThreads)
-        out[e] = (uint16_t)mask[e];
-}
-
-__host__ __device__ inline int64_t chunks_of(int64_t T) { return (T + kChunk - 1) / kChunk; }
-// The rows of sums follow the masks, from 16 bytes on.
-__host__ __device__ inline int64_t mask_bytes(int64_t T, int64_t E)
-{
-    return (chunks_of(T) * E * 2 + 15) & ~(int64_t)15;
+    const int ld = mask_row(a.E);
+    uint16_t *out = static_cast<uint16_t *>(a.workspace) + (int64_t)blockIdx.x * ld;
+    for (int e = tid; e < ld; e += kThreads)
+        out[e] = e < a.E ? (uint16_t)mask[e] : 0;
 }
 
 // Counts of every kSuper tokens, [T/1024][E].
@@ -268,7 +345,7 @@ __global__ void __launch_bounds__(256) route_sums_kernel(const RouteArgs a)
     for (int e = threadIdx.x; e < a.E; e += 256) {
         int s = 0;
         for (int64_t c = first; c < first + PER && c < chunks; ++c)
-            s += __popc(masks[c * a.E + e]);
+            s += __popc(masks[c * mask_row(a.E) + e]);
         sums[(int64_t)blockIdx.x * a.E + e] = s;
     }
 }
@@ -284,38 +361,57 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteArgs a
         reinterpret_cast<const int *>(static_cast<const char *>(a.workspace) + mask_bytes(a.T, a.E));
     const int tid = threadIdx.x, E = a.E;
     const int64_t chunks = chunks_of(a.T), first = (int64_t)blockIdx.x * PER;
-    for (int e = tid; e < E; e += kThreads)
+    const int ld = mask_row(E);
+    for (int e = tid; e < E; e += kThreads) {
         total[e] = before[e] = 0;
+        uint64_t m = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (first + i < chunks)
+                m |= (uint64_t)masks[(first + i) * ld + e] << (kChunk * i);
+        mask[e] = m;
+    }
     __syncthreads();
-    // threads: `parts` rows at a time, one expert each
-    const int width = (E + 63) & ~63, parts = kThreads / width, e = tid % width, part = tid / width;
-    if (part < parts && e < E) {
-        int all = 0, low = 0;
+    // Masks are added up eight experts (16 bytes) a thread, as many rows at a time as
+    // there are threads.
+    const int width = ld / 8, rows = kThreads / width, row = tid / width, e8 = tid % width * 8;
+    const int64_t own = first / (kSuper / kChunk);  // this workgroup's row of sums
+    if (row < rows) {
+        int all[8] = {}, low[8] = {};
+        auto add = [&](int64_t c, bool to_all) {
+            const u32x4_v m = *reinterpret_cast<const u32x4_v *>(masks + c * ld + e8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int n = __popc(i & 1 ? m[i / 2] >> 16 : m[i / 2] & 0xffffu);
+                all[i] += to_all ? n : 0;
+                low[i] += c < first ? n : 0;
+            }
+        };
         if (flat) {
-            for (int64_t c = part; c < chunks; c += parts) {
-                const int n = __popc(masks[c * E + e]);
-                all += n;
-                low += c < first ? n : 0;
-            }
+#pragma unroll 4
+            for (int64_t c = row; c < chunks; c += rows)
+                add(c, true);
         } else {
-            const int64_t supers = (a.T + kSuper - 1) / kSuper, own = first / (kSuper / kChunk);
-            for (int64_t s = part; s < supers; s += parts) {
-                const int n = sums[s * E + e];
-                all += n;
-                low += s < own ? n : 0;
+            for (int64_t c = own * (kSuper / kChunk) + row; c < first; c += rows)
+                add(c, false);
+            const int64_t supers = (a.T + kSuper - 1) / kSuper;
+#pragma unroll 2
+            for (int64_t s = row; s < supers; s += rows)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int n = e8 + i < E ? sums[s * E + e8 + i] : 0;
+                    all[i] += n;
+                    low[i] += s < own ? n : 0;
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (e8 + i < E) {
+                if (all[i])
+                    atomicAdd(&total[e8 + i], all[i]);
+                if (low[i])
+                    atomicAdd(&before[e8 + i], low[i]);
             }
-            for (int64_t c = own * (kSuper / kChunk) + part; c < first; c += parts)
-                low += __popc(masks[c * E + e]);
-        }
-        atomicAdd(&total[e], all);
-        atomicAdd(&before[e], low);
-        if (part == 0) {
-            uint64_t m = 0;
-            for (int i = 0; i < PER; ++i)
-                if (first + i < chunks)
-                    m |= (uint64_t)masks[(first + i) * E + e] << (kChunk * i);
-            mask[e] = m;
-        }
     }
     scan_counts(total, E);
     if (blockIdx.x == 0)
