@@ -413,10 +413,16 @@ def _same_device(first: torch.Tensor, *rest) -> int:
     return dev
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_fns: dict = {}
+
+
 def _call(name: str, dev: int, *args) -> None:
     """Calls a library function on the current stream of device `dev`."""
-    fn = getattr(_lib or lib(), name)
-    if dev == torch.cuda.current_device():
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    if dev == _current_device():
         st = fn(*args, _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream)
     else:
         with torch.cuda.device(dev):
@@ -431,11 +437,11 @@ def _choice(table: dict, value, name: str) -> int:
     return table[value]
 
 
-def _output(out, shape, dtype, dev):
-    """`out` checked, or a new tensor."""
+def _output(out, shape, dtype, dev, like):
+    """`out` checked, or a new tensor where `like` is."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
-    if tuple(out.shape) != shape or out.dtype not in _OUT or not out.is_contiguous() \
+        return like.new_empty(shape, dtype=dtype)
+    if out.shape != shape or out.dtype not in _OUT or not out.is_contiguous() \
             or out.get_device() != dev:
         raise ValueError(f"out must be a contiguous bfloat16, float16 or float32 tensor of shape {shape} "
                          "on the inputs' device")
@@ -479,12 +485,12 @@ def fp8_linear(xq: torch.Tensor, x_scale: torch.Tensor, wq: torch.Tensor, w_scal
     if K == 0 or K % 128 or wq.shape[1] != K:
         raise ValueError(f"xq [{M}, {K}] and wq {tuple(wq.shape)} must share K, a multiple of 128")
     if x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32 \
-            or tuple(x_scale.shape) != (M, K // 128) or tuple(w_scale.shape) != ((N + 127) // 128, K // 128):
+            or x_scale.shape != (M, K // 128) or w_scale.shape != ((N + 127) // 128, K // 128):
         raise ValueError(f"scales must be float32 [{M}, {K // 128}] and [{(N + 127) // 128}, {K // 128}]")
     dev = _same_device(xq, xq, x_scale, wq, w_scale)
     if dtype not in _OUT:
         raise ValueError("dtype must be bfloat16, float16 or float32")
-    out = _output(out, (M, N), dtype, dev)
+    out = _output(out, (M, N), dtype, dev, x_scale)
     _call("ternary_fp8_linear", dev, xq.data_ptr(), x_scale.data_ptr(), wq.data_ptr(), w_scale.data_ptr(),
           M, N, K, out.data_ptr(), _OUT[out.dtype])
     return out
@@ -514,7 +520,7 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
         raise ValueError("logits must be a 2-D bfloat16, float16 or float32 tensor")
     sc = _choice(SCORES, score, "score")
     T, E = logits.shape
-    if bias is not None and (bias.dtype != torch.float32 or tuple(bias.shape) != (E,)):
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,)):
         raise ValueError(f"bias must be a float32 tensor [{E}]")
     dev = _same_device(logits, logits, bias)
     if top_groups is None:
@@ -528,7 +534,7 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
     weights = torch.empty((T, top_k), dtype=torch.float32, device=d)
     offsets = torch.empty(E + 1, dtype=torch.int32, device=d)
     order = torch.empty(T * top_k, dtype=torch.int32, device=d)
-    slots = torch.empty((T, top_k), dtype=torch.int32, device=d)
+    slots = torch.empty_like(ids)
     ws = torch.empty(need, dtype=torch.uint8, device=d).data_ptr() if need else None
     _call("ternary_route", dev, logits.data_ptr(), dt, T, E, bias.data_ptr() if bias is not None else None,
           sc, groups, top_groups, top_k, 1 if renormalize else 0, scale, ids.data_ptr(),
@@ -537,10 +543,12 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
 
 
 def _check_routing(r: Routing):
-    T, k = r.ids.shape
-    if not all(t.dtype == torch.int32 for t in (r.ids, r.offsets, r.order, r.slots)) \
-            or r.weights.dtype != torch.float32 or tuple(r.order.shape) != (T * k,) \
-            or r.slots.shape != r.ids.shape or r.weights.shape != r.ids.shape:
+    ids, weights, offsets, order, slots = r
+    i32, shape = torch.int32, ids.shape
+    T, k = shape
+    if ids.dtype is not i32 or offsets.dtype is not i32 or order.dtype is not i32 or slots.dtype is not i32 \
+            or weights.dtype is not torch.float32 or order.shape != (T * k,) or slots.shape != shape \
+            or weights.shape != shape:
         raise ValueError("routing must hold int32 ids and slots [T, k], offsets [E + 1], order [T * k] "
                          "and float32 weights [T, k]")
     return T, k
@@ -563,7 +571,7 @@ def linear_experts(xq: torch.Tensor, x_scale: torch.Tensor, packed: torch.Tensor
     R, (n, Kp) = T * k, xq.shape
     if K is None:
         K = Kp
-    if Kp != (K + 127) // 128 * 128 or tuple(x_scale.shape) != (n, Kp // 128):
+    if Kp != (K + 127) // 128 * 128 or x_scale.shape != (n, Kp // 128):
         raise ValueError(f"xq [{n}, {Kp}] and x_scale {tuple(x_scale.shape)} do not match K={K}")
     by = _choice(ROWS, rows, "rows")
     if n != (R if by else T):
@@ -579,12 +587,12 @@ def linear_experts(xq: torch.Tensor, x_scale: torch.Tensor, packed: torch.Tensor
     if packed.dtype != torch.uint8 or packed.dim() < 1 or packed.shape[0] != E \
             or packed.numel() != E * tiled_bytes(N, K):
         raise ValueError(f"packed must be uint8 [{E}, ...] with {tiled_bytes(N, K)} bytes an expert")
-    if tuple(routing.offsets.shape) != (E + 1,):
+    if routing.offsets.shape != (E + 1,):
         raise ValueError(f"routing.offsets must hold {E + 1} values")
     dev = _same_device(xq, xq, x_scale, packed, scale, routing.offsets, routing.order)
     if dtype not in _OUT:
         raise ValueError("dtype must be bfloat16, float16 or float32")
-    out = _output(out, (R, N), dtype, dev)
+    out = _output(out, (R, N), dtype, dev, x_scale)
     _call("ternary_linear_experts", dev, xq.data_ptr(), x_scale.data_ptr(), n, packed.data_ptr(),
           scale.data_ptr(), E, N, K, g, routing.offsets.data_ptr(), routing.order.data_ptr(), R, k, by,
           out.data_ptr(), _OUT[out.dtype])
@@ -603,10 +611,10 @@ def combine(y: torch.Tensor, routing: Routing, add: torch.Tensor | None = None,
     R, N = y.shape
     if R != T * k:
         raise ValueError(f"y must have {T * k} rows")
-    if add is not None and (add.dtype != y.dtype or tuple(add.shape) != (T, N)):
+    if add is not None and (add.dtype != y.dtype or add.shape != (T, N)):
         raise ValueError(f"add must match y's dtype and have shape [{T}, {N}]")
     dev = _same_device(y, y, routing.slots, routing.weights, add)
-    out = _output(out, (T, N), y.dtype, dev)
+    out = _output(out, (T, N), y.dtype, dev, y)
     if out.dtype != y.dtype:
         raise ValueError("out must have y's dtype")
     _call("ternary_combine", dev, y.data_ptr(), dt, R, N, routing.slots.data_ptr(),

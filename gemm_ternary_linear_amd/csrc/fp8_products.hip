@@ -257,7 +257,7 @@ __device__ __forceinline__ void load_group_scales(const uint16_t *row, int b0, i
 
 // TERN: ternary weights of experts (G: with group scales).
 template <bool TERN, bool G, int MT, int FN>
-__global__ void __launch_bounds__(kThreads, 4) thin_kernel(const Fp8Product p, int ks)
+__global__ void __launch_bounds__(kThreads, FN * MT <= 8 ? 4 : 2) thin_kernel(const Fp8Product p, int ks)
 {
     constexpr int U = thin_chunk(MT);
     typedef float u_t __attribute__((ext_vector_type(U)));  // scales of a chunk
@@ -332,8 +332,10 @@ __global__ void __launch_bounds__(kThreads, 4) thin_kernel(const Fp8Product p, i
     const int c0 = cg ^ (col & 7), c1 = (cg + (TERN ? 2 : 4)) ^ (col & 7);
     lds_u4 *const lx = (lds_u4 *)sx + wave * (U * MT * 128);
     const int xa = (col >> 3) * 64 + (col & 7) * 8;
-    constant_float *wsp = TERN ? nullptr : (constant_float *)(p.w_scale + (int64_t)min(n0 / kFp8Block, (p.N - 1) / kFp8Block) * nb);
-    static_assert(FN <= 4, "a wave's channels share w's scales");
+    constant_float *wsp[FN];  // w's scales of each fragment (16 channels are in one block)
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+        wsp[i] = TERN ? nullptr : (constant_float *)(p.w_scale + (int64_t)(min(n0 + 16 * i, p.N - 1) / kFp8Block) * nb);
 
     f32x4_t acc[FN][MT];
 #pragma unroll
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 4) thin_kernel(const Fp8Product p, i
 
     // Blocks past the last load that again, and count with scale 0.
     for (int b0 = kpart * U; b0 < nb; b0 += ks * U) {
-        float ws[U];
+        float ws[FN][U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -367,8 +369,10 @@ __global__ void __launch_bounds__(kThreads, 4) thin_kernel(const Fp8Product p, i
         }
         if constexpr (!TERN)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                ws[u] = wsp[min(b0 + u, nb - 1)];
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    ws[i][u] = wsp[i][min(b0 + u, nb - 1)];
         if constexpr (G)
             if (lane < 16 * FN) {  // a channel a lane
                 uint16_t v[U];
@@ -422,10 +426,10 @@ __global__ void __launch_bounds__(kThreads, 4) thin_kernel(const Fp8Product p, i
             for (int j = 0; j < MT; ++j) {
                 const u32x4_v x0 = lx[(u * MT + j) * 128 + xa + c0], x1 = lx[(u * MT + j) * 128 + xa + c1];
                 const i32x8_v xv = TERN ? odd_even(x0, x1) : join(x0, x1);
-                const float f = TERN ? xs[j][u] : xs[j][u] * ws[u];
 #pragma unroll
                 for (int i = 0; i < FN; ++i) {
                     const f32x4_t d = mfma<TERN>(a[i][u & 1], xv);
+                    const float f = TERN ? xs[j][u] : xs[j][u] * ws[i][u];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         acc[i][j][k] += d[k] * (G ? f * gs[i][k] : f);
@@ -478,12 +482,43 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
     return hipGetLastError();
 }
 
-// One fragment of channels a wave where two would leave compute units without a workgroup.
+// Fragments of 16 channels a wave holds: F with the fewest rounds of F over the
+// compute units, the larger of two (it reads x less often).  18944 x 4096 at 45
+// rows: F = 5 19.2 us, 3 22.6, 2 24.7, 1 26.5; 8192 x 4096: F = 2 10.0, 1 12.6, 5
+// 17.4; 4096 x 4096: F = 1 8.0, 2 9.7.  Where a chunk is long (one fragment of
+// rows) or x takes much of LDS (four) F = 2 is the most that pays (8 rows
+// of 18944 x 4096: F = 1 to 3 about 20 us, 5 31; 64 rows: F = 2 28.3, 5 33.1).
+inline int thin_fragments(int64_t frags, int most)
+{
+    const int64_t cus = device_cus();
+    int best = 1;
+    int64_t least = INT64_MAX;
+    for (int f = 1; f <= most; ++f) {
+        const int64_t rounds = (frags + f * cus - 1) / (f * cus) * f;
+        if (rounds <= least && f != 4)
+            least = rounds, best = f;
+    }
+    return best;
+}
+
 template <bool TERN, bool G, int MT>
 hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 {
-    return (p.N + 15) / 16 * tiles < 1024 ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
-                                          : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
+    const int64_t frags = (p.N + 15) / 16 * tiles;
+    if constexpr (TERN) {
+        return frags < 1024 ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
+                            : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
+    } else if constexpr (MT == 1 || MT == 4) {
+        return frags <= device_cus() ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
+                                     : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
+    } else {
+        switch (thin_fragments(frags, 5)) {
+        case 1: return launch_thin<TERN, G, MT, 1>(p, tiles, stream);
+        case 2: return launch_thin<TERN, G, MT, 2>(p, tiles, stream);
+        case 3: return launch_thin<TERN, G, MT, 3>(p, tiles, stream);
+        default: return launch_thin<TERN, G, MT, 5>(p, tiles, stream);
+        }
+    }
 }
 
 // Rows in tiles of 16 MT.
@@ -560,9 +595,7 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
         tn = in / rows;
     }
     const int n0 = tn * TN;
-    // dense: the last tile ends at M, so that every row of a tile exists (rows of
-    // two tiles are computed by both, to the same bits)
-    int e = 0, r0 = min(tm * TM, p.M - TM), r1 = r0 + TM;
+    int e = 0, r0 = tm * TM, r1 = min(p.M, r0 + TM);
     if constexpr (TERN)
         if (!find_tile<TM>(p.offsets, p.E, p.M, tm, e, r0, r1))
             return;
@@ -576,15 +609,14 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
         }
         return row;
     };
-    // Sources.  Gathered rows of x and the experts' blocks have pointers of
-    // their own; a dense tile is one resource, each thread's rows a uniform
-    // distance apart.
+    // Sources (rows and channels past the last repeat it).  Gathered rows of x and the
+    // experts' blocks have pointers of their own, a dense tile is one resource
+    // with 32-bit offsets.
     constexpr int RS = THREADS / 8;        // rows between a thread's chunks of x
     const int rowbytes = nb * kFp8Block;   // at most 2^20
     static_assert(RS % 8 == 0, "the same chunk of each row");
     const uint8_t *xsrc[XI], *wsrc = nullptr;
-    int woff[WI];
-    const int off = (tid >> 3) * rowbytes + 16 * ((tid & 7) ^ swz(tid >> 3));
+    int xoff[XI], woff[WI];
     __amdgpu_buffer_rsrc_t xr, wr;
     if constexpr (TERN) {
 #pragma unroll
@@ -595,8 +627,11 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
         const int blk = min(n0 / 16 + (tid >> 5), (p.N + 15) / 16 - 1);
         wsrc = p.w + ((int64_t)e * ((p.N + 15) / 16) + blk) * ((nb + 1) / 2) * kTileBytes + 16 * (tid & 31);
     } else {
-        xr = make_rsrc(p.x + (int64_t)r0 * rowbytes, (uint32_t)(TM * rowbytes));
-        const int chans = min(TN, p.N - n0);  // (those past the last repeat it)
+        const int rows = r1 - r0, chans = min(TN, p.N - n0);
+        xr = make_rsrc(p.x + (int64_t)r0 * rowbytes, (uint32_t)(rows * rowbytes));
+#pragma unroll
+        for (int i = 0; i < XI; ++i)
+            xoff[i] = min((tid >> 3) + i * RS, rows - 1) * rowbytes + 16 * ((tid & 7) ^ swz(tid >> 3));
         wr = make_rsrc(p.w + (int64_t)n0 * rowbytes, (uint32_t)(chans * rowbytes));
 #pragma unroll
         for (int i = 0; i < WI; ++i)
@@ -606,21 +641,21 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
     const uint16_t *gsrc = G ? p.t_scale + ((int64_t)e * p.N + min(n0 + tid, p.N - 1)) * p.ngroups : nullptr;
     const int gsteps = G ? p.group / kFp8Block : 1;
 
-    auto issue = [&](auto S, int b) {
+    // One of the NP loads into a stage that a thread issues for step b.
+    constexpr int NP = XI + WI;
+    auto issue = [&](auto S, int b, int q) {
         constexpr int s = decltype(S)::value;
-#pragma unroll
-        for (int i = 0; i < XI; ++i) {
-            lds_u4 *to = lx[s] + i * THREADS + wave * 64;
+        if (q < XI) {
+            lds_u4 *to = lx[s] + q * THREADS + wave * 64;
             if constexpr (TERN)
-                load_to_lds(xsrc[i] + b * kFp8Block, to);
+                load_to_lds(xsrc[q < XI ? q : 0] + b * kFp8Block, to);
             else
-                load_to_lds(xr, to, off, i * RS * rowbytes + b * kFp8Block);
-        }
-#pragma unroll
-        for (int i = 0; i < WI; ++i) {
+                load_to_lds(xr, to, xoff[q < XI ? q : 0], b * kFp8Block);
+        } else {
+            const int i = q - XI;
             lds_u4 *to = lw[s] + i * THREADS + wave * 64;
             if constexpr (!TERN)
-                load_to_lds(wr, to, woff[i], b * kFp8Block);
+                load_to_lds(wr, to, woff[q >= XI ? i : 0], b * kFp8Block);
             else if (WCH % THREADS == 0 || wave * 64 < WCH)
                 load_to_lds(wsrc + (int64_t)b * (kTileBytes / 2), to);
         }
@@ -730,7 +765,11 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
     // result of the fragment before, so that neither waits for the other.  The
     // waves meet two fragments before the end, once the stage is read and the next one is there:
     // from then on this stage takes step b + 2, and the next step's first
-    // operands are read behind the last fragments' matrix instructions.
+    // operands are read behind the last fragments' matrix instructions.  The
+    // stage's loads are spread from there over the first fragments of the next
+    // step: issued together they hold up the waves, whose turns in the load unit
+    // come one after another.
+    constexpr int ROWS = FN >= 8 ? 4 : 1, LATE = NP / 2 < ROWS ? NP / 2 : ROWS, EARLY = NP - LATE;
     auto step = [&](auto S, int b) {
         constexpr int s = decltype(S)::value;
         constexpr std::integral_constant<int, s ^ 1> T;
@@ -746,7 +785,6 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
                 gnew = sg[b & 7][(wn * FN + i) * 4 + g];
             if (i == FN - 2) {
                 meet();
-                issue(S, min(b + 2, nb - 1));
                 if constexpr (s == 0) {
                     // scales ahead: loaded at the first step of four, put into LDS at the third
                     if (b & 2)
@@ -770,6 +808,13 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
                     gs[i & 1] = gnew;
                 const int m = n >= LAG ? n - LAG : n - LAG + FN * FM;
                 scale_add(m, n >= LAG ? f : fp);
+                if (j == 1 && i < LATE)
+                    issue(T, min(b + 1, nb - 1), EARLY + i);
+                if (i >= FN - 2)
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+                        if (q < EARLY && q % (2 * FM) == (i - (FN - 2)) * FM + j)
+                            issue(S, min(b + 2, nb - 1), q);
                 asm volatile("" : "+v"(acc[m / FM][m % FM]));  // (the same, down)
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -785,9 +830,13 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
     // Every step loads the stage of the step after the next; the last ones load the
     // last step again, into a stage that is not read (a branch there, or a second exit of the loop, had
     // the compiler copy the step).
-    issue(std::integral_constant<int, 0>(), 0);
-    issue(std::integral_constant<int, 1>(), min(1, nb - 1));
+#pragma unroll
+    for (int q = 0; q < NP; ++q)
+        issue(std::integral_constant<int, 0>(), 0, q);
     meet();
+#pragma unroll
+    for (int q = 0; q < EARLY; ++q)
+        issue(std::integral_constant<int, 1>(), min(1, nb - 1), q);
     read_w(std::integral_constant<int, 0>(), 0);
     read_w(std::integral_constant<int, 0>(), 1);
     read_f(0);
@@ -852,6 +901,23 @@ int64_t expert_tiles(const Fp8Product &p, int rows)
 
 }  // namespace
 
+namespace {
+
+// Expected time of n tiles in rounds of `most`, as a multiple of a round's: between
+// whole rounds and an even spread.
+double rounds_of(int64_t n, int64_t most)
+{
+    return ((double)((n + most - 1) / most) + (n > most ? (double)n / most : 1.0)) / 2;
+}
+
+}  // namespace
+
+// Which kernel: the least of what each is expected to take, from its time a
+// block of K (us, measured over M = 64 .. 2048 at 18944 x 4096, 4096 x 4096 and 1024 x 8192;
+// the estimates are within 25 % there).  Measured sides, us: 64 rows of 4096 x 4096 streamed 9.3,
+// tiles of 64 rows 15; of 18944 x 4096 28 and 23.5; 192 rows of 1024 x 8192 12.7 and 25; 384 rows
+// of 18944 x 4096 tiles of 64 52, 128 39, 256 56; 1024 rows 124, 97, 110; 2048 rows
+// 218, 180, 172.
 hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
 {
     if (p.M <= 16)
@@ -860,9 +926,19 @@ hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
         return launch_thin<false, 2>(p, 1, stream);
     if (p.M <= 48)
         return launch_thin<false, 3>(p, 1, stream);
-    if (p.M < 256)
-        return launch_thin<false, 4>(p, (p.M + 63) / 64, stream);
-    return launch_tiles<false, Tile<256, 256, 2, 4>>(p, (p.M + 255) / 256, stream);
+    const int64_t cus = device_cus(), m64 = (p.M + 63) / 64, m128 = (p.M + 127) / 128, m256 = (p.M + 255) / 256;
+    const int64_t n128 = ((int64_t)p.N + 127) / 128, n256 = ((int64_t)p.N + 255) / 256, frags = m64 * ((p.N + 15) / 16);
+    const double t_thin = 1.0 + p.nb * (frags <= cus ? 0.178 : 0.237 * rounds_of((frags + 1) / 2, cus));
+    const double t_64 = p.nb * (m64 * n128 <= cus ? 0.5 : 0.85 * rounds_of(m64 * n128, 2 * cus));
+    const double t_128 = p.nb * (m128 * n128 <= cus ? 0.72 : 1.2 * rounds_of(m128 * n128, 2 * cus));
+    const double t_256 = p.nb * 1.75 * rounds_of(m256 * n256, cus);
+    if (t_thin <= t_64 && t_thin <= t_128 && t_thin <= t_256)
+        return launch_thin<false, 4>(p, m64, stream);
+    if (t_64 <= t_128 && t_64 <= t_256)
+        return launch_tiles<false, Tile<128, 64, 2, 2>>(p, m64, stream);
+    if (t_128 <= t_256)
+        return launch_tiles<false, Tile<128, 128, 2, 2>>(p, m128, stream);
+    return launch_tiles<false, Tile<256, 256, 2, 4>>(p, m256, stream);
 }
 
 hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream)
@@ -871,7 +947,7 @@ hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream)
         return launch_thin<true, 1>(p, expert_tiles(p, 16), stream);
     if (p.M <= 32 * p.E)
         return launch_thin<true, 2>(p, expert_tiles(p, 32), stream);
-    return launch_tiles<true, Tile<256, 128, 4, 2>>(p, expert_tiles(p, 128), stream);
+    return launch_tiles<true, Tile<128, 128, 2, 2>>(p, expert_tiles(p, 128), stream);
 }
 
 }  // namespace ternary
