@@ -154,18 +154,19 @@ __device__ __forceinline__ void put4(const Fp8Product &p, int row, int ch, f32x4
         put4<TERNARY_FP32>(p, row, ch, s);
 }
 
-// Waits for everything this wave has loaded (LDS reads, and loads into LDS among
-// them), then for the workgroup's other waves.
+// Waits for all but the last N of this wave's loads from memory (those into LDS
+// among them) and for its LDS reads, then for the workgroup's other waves.
+template <int N>
 __device__ __forceinline__ void meet()
 {
+    static_assert(N >= 0 && N < 64);
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4);  // vmcnt(N) lgkmcnt(0)
     asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
 
 typedef __attribute__((address_space(3))) u32x4_v lds_u4;
-typedef __attribute__((address_space(3))) u32x2_v lds_u2;
 typedef __attribute__((address_space(3))) void lds_void;
 
 // One memory-to-LDS load: 16 bytes a lane from `src`, to lds + 16 * lane.
@@ -533,11 +534,15 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 
 // ---------------------------------------------------------------- many rows
 
-template <int TN_, int TM_, int WN_, int WM_>
+// Tiles of TN channels x TM rows by WN x WM waves, NS stages deep.
+template <int TN_, int TM_, int WN_, int WM_, int NS_ = 2>
 struct Tile {
-    static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_;
+    static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, NS = NS_;
+    static_assert(NS == 2 || NS == 4);
     static constexpr int THREADS = WN * WM * 64;
     static constexpr int FN = TN / WN / 16, FM = TM / WM / 16;  // fragments of a wave
+    // waves a SIMD has registers for: one workgroup's, of 512 threads two
+    static constexpr int WAVES = THREADS / 256;
 };
 
 // Values b0 .. b0 + 3 of a row of n (past its end the last) that a whole workgroup reads.
@@ -549,24 +554,27 @@ __device__ __forceinline__ f32x4_t load_scales_uniform(const float *row, int b0,
 
 // G: group-scaled ternary weights.
 template <bool TERN, bool G, int DT, class C>
-__global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
+__global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Product p)
 {
-    constexpr int TN = C::TN, TM = C::TM, FN = C::FN, FM = C::FM, THREADS = C::THREADS;
+    constexpr int TN = C::TN, TM = C::TM, FN = C::FN, FM = C::FM, THREADS = C::THREADS, NS = C::NS;
     constexpr int XI = TM * 8 / THREADS;                      // x loads of a thread and stage
     constexpr int WCH = TERN ? TN * 2 : TN * 8;               // 16-byte chunks of w in a stage
     constexpr int WI = (WCH + THREADS - 1) / THREADS;
     constexpr int QB = TERN ? 1 : (TN + 127) / 128;           // blocks of channels with scales of their own
     static_assert(TM * 8 % THREADS == 0 && (WCH % THREADS == 0 || WI == 1) && TM <= THREADS && TN <= THREADS);
-    // one object per stage: a load into one stage is then known not to touch the other
-    __shared__ __attribute__((aligned(16))) u32x4_v sx0[TM * 8], sx1[TM * 8], sw0[WCH], sw1[WCH];
-    // scales of eight steps: x's (times w's for 8-bit weights), a lane's FM
-    // rows together, and a group's channels'.  Each is read by one load: a pair of loads that the
-    // compiler merges loses the object it reads, and with it would wait for every stage in flight.
+    // One object per stage (x, then w): a load into one stage is then known not to
+    // touch the others.
+    constexpr int STAGE = TM * 8 + WCH, S2 = NS > 2 ? STAGE : 1;
+    __shared__ __attribute__((aligned(16))) u32x4_v st0[STAGE], st1[STAGE], st2[S2], st3[S2];
+    lds_u4 *const lx[4] = {(lds_u4 *)st0, (lds_u4 *)st1, (lds_u4 *)st2, (lds_u4 *)st3};
+    lds_u4 *const lw[4] = {lx[0] + TM * 8, lx[1] + TM * 8, lx[2] + (NS > 2 ? TM * 8 : 0), lx[3] + (NS > 2 ? TM * 8 : 0)};
+    // Scales of eight steps: x's (times w's for 8-bit weights), a lane's FM rows
+    // together, then a group's channels', a lane's FN fragments together.  They are read
+    // and written right behind the waves' meeting: the compiler waits for every load into
+    // LDS that is under way before it touches an object that none of them writes.
     typedef float fm_t __attribute__((ext_vector_type(FM)));
-    __shared__ __attribute__((aligned(16))) fm_t sf[QB][8][TM / FM];
-    __shared__ __attribute__((aligned(16))) f32x4_t sg[G ? 8 : 1][G ? TN / 4 : 1];
-
-    lds_u4 *const lx[2] = {(lds_u4 *)sx0, (lds_u4 *)sx1}, *const lw[2] = {(lds_u4 *)sw0, (lds_u4 *)sw1};
+    constexpr int SF = QB * TM, SL = SF + (G ? TN : 0);
+    __shared__ __attribute__((aligned(16))) float sf[8 * SL];
 
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -660,38 +668,49 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
                 load_to_lds(wsrc + (int64_t)b * (kTileBytes / 2), to);
         }
     };
-    f32x4_t fx = {0.f, 0.f, 0.f, 0.f}, fw[QB], gv = fx;
-    auto load_factors = [&](int b0) {  // of steps b0 .. b0 + 3
+    // The scales of four steps in registers (a row of x, and a channel, a thread).
+    // (Group scales as loaded: a conversion here would wait for them, and with them
+    // for all loads before.)
+    struct Factors {
+        f32x4_t x, w[QB];
+        uint32_t g[4];
+    };
+    auto load_factors = [&](int b0) -> Factors {
+        Factors r = {};
         if (wave < TM / 64 && b0 < nb) {
             float v[4];
             load_scales<4>(fsrc, b0, nb, v);
-            fx = f32x4_t{v[0], v[1], v[2], v[3]};
+            r.x = f32x4_t{v[0], v[1], v[2], v[3]};
         }
         if constexpr (!TERN)
 #pragma unroll
             for (int q = 0; q < QB; ++q)
-                fw[q] = load_scales_uniform(p.w_scale + (int64_t)min(n0 / 128 + q, (p.N - 1) / 128) * nb, b0, nb);
+                r.w[q] = load_scales_uniform(p.w_scale + (int64_t)min(n0 / 128 + q, (p.N - 1) / 128) * nb, b0, nb);
         if constexpr (G)
-            if (wave < TN / 64)
+            if (wave < TN / 64) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    gv[i] = channel_scale(gsrc[min(b0 + i, nb - 1) / gsteps]);
+                    r.g[i] = gsrc[min((b0 + i) / gsteps, p.ngroups - 1)];
+            }
+        return r;
     };
     // row r = 16 (FM u + j) + c of the tile: entry j of (u, c)
     const int fpos = ((tid / (16 * FM)) * 16 + (tid & 15)) * FM + (tid >> 4) % FM;
-    auto store_factors = [&](int b0) {
-        if (wave < TM / 64)
+    // channel 16 (FN u + i) + 4 g + k: entry 4 i + k of (u, g)
+    const int gpos = ((tid / (16 * FN)) * 4 + (tid >> 2) % 4) * 4 * FN + (tid >> 4) % FN * 4 + tid % 4;
+    auto store_factors = [&](const Factors &r, int b0) {
 #pragma unroll
-            for (int q = 0; q < QB; ++q)
+        for (int i = 0; i < 4; ++i) {
+            if (wave < TM / 64)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    reinterpret_cast<float *>(sf[q][(b0 + i) & 7])[fpos] = TERN ? fx[i] : fx[i] * fw[q][i];
-        if constexpr (G)
-            if (wave < TN / 64)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    reinterpret_cast<float *>(sg[(b0 + i) & 7])[tid] = gv[i];
+                for (int q = 0; q < QB; ++q)
+                    sf[((b0 + i) & 7) * SL + q * TM + fpos] = TERN ? r.x[i] : r.x[i] * r.w[q][i];
+            if constexpr (G)
+                if (wave < TN / 64)
+                    sf[((b0 + i) & 7) * SL + SF + gpos] = channel_scale((uint16_t)r.g[i]);
+        }
     };
+    Factors next;
 
     f32x4_t acc[FN][FM];
 #pragma unroll
@@ -714,11 +733,13 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
     // fragments by one load), all of x's, and the scales.
     u32x4_v rw[2][2], rx[FM][2];
     fm_t fn, f, fp;          // the next step's, this step's, the last one's
-    // matrix results not yet scaled, and two fragments' channels' scales.  A
+    // matrix results not yet scaled, and the fragments' channels' scales.  A
     // result is scaled behind the second matrix instruction after its own: it is there by then.
     constexpr int LAG = 2;
     static_assert(FM >= LAG && FN * FM % 4 == 0);
-    f32x4_t d[4], gs[2];
+    f32x4_t d[4];
+    typedef float g_t __attribute__((ext_vector_type(G ? 4 * FN : 4)));
+    g_t gn, gs, gp;  // (the next step's, this step's, the last one's)
     auto read_w = [&](auto S, int i) {
         constexpr int s = decltype(S)::value;
         if constexpr (TERN) {
@@ -734,7 +755,12 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
         rx[j][0] = lx[s][xa + j * 128 + c0];
         rx[j][1] = lx[s][xa + j * 128 + c1];
     };
-    auto read_f = [&](int b) { fn = sf[TERN ? 0 : (wn * FN * 16) / 128][b & 7][wm * 16 + col]; };
+    auto read_f = [&](int b) {
+        fn = *reinterpret_cast<const fm_t *>(
+            sf + (b & 7) * SL + (TERN ? 0 : (wn * FN * 16) / 128 * TM) + (wm * 16 + col) * FM);
+        if constexpr (G)
+            gn = *reinterpret_cast<const g_t *>(sf + (b & 7) * SL + SF + (wn * 4 + g) * 4 * FN);
+    };
     u32x2_v odd_codes = {0, 0};  // of the second fragment of two
     auto w_operand = [&](int i) -> i32x8_v {
         if constexpr (TERN) {
@@ -754,17 +780,17 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
             return join(rw[i & 1][0], rw[i & 1][1]);
         }
     };
-    auto scale_add = [&](int n, const fm_t &by) {  // result n of a step
+    auto scale_add = [&](int n, const fm_t &by, bool last) {  // result n of this step, or of the last one
         const int i = n / FM, j = n % FM;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            acc[i][j][k] += d[n & 3][k] * (G ? by[j] * gs[i & 1][k] : by[j]);
+            acc[i][j][k] += d[n & 3][k] * (G ? by[j] * (last ? gp : gs)[G ? 4 * i + k : 0] : by[j]);
     };
 
     // Step b, from stage s.  Each matrix instruction is followed by the scaling of a
     // result of the fragment before, so that neither waits for the other.  The
     // waves meet two fragments before the end, once the stage is read and the next one is there:
-    // from then on this stage takes step b + 2, and the next step's first
+    // from then on this stage takes step b + NS, and the next step's first
     // operands are read behind the last fragments' matrix instructions.  The
     // stage's loads are spread from there over the first fragments of the next
     // step: issued together they hold up the waves, whose turns in the load unit
@@ -772,27 +798,32 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
     constexpr int ROWS = FN >= 8 ? 4 : 1, LATE = NP / 2 < ROWS ? NP / 2 : ROWS, EARLY = NP - LATE;
     auto step = [&](auto S, int b) {
         constexpr int s = decltype(S)::value;
-        constexpr std::integral_constant<int, s ^ 1> T;
+        constexpr std::integral_constant<int, (s + 1) % NS> T;       // the next step's stage
+        constexpr std::integral_constant<int, (s + NS - 1) % NS> L;  // the last step's
         static_assert(FN % 2 == 0 && FN >= 4);
         i32x8_v x[FM];
         fp = f;
         f = fn;
+        gp = gs;
+        gs = gn;
 #pragma unroll
         for (int i = 0; i < FN; ++i) {
             const i32x8_v a = w_operand(i);
-            f32x4_t gnew;
-            if constexpr (G)
-                gnew = sg[b & 7][(wn * FN + i) * 4 + g];
             if (i == FN - 2) {
-                meet();
-                if constexpr (s == 0) {
-                    // scales ahead: loaded at the first step of four, put into LDS at the third
-                    if (b & 2)
-                        store_factors(b + 2);
-                    else
-                        load_factors(b + 4);
-                }
+                meet<(NS - 2) * NP>();
                 read_f(b + 1);
+                // scales ahead: loaded at the first step of four, put into LDS at the third
+                if constexpr (NS == 4) {
+                    if (s == 0)
+                        next = load_factors(b + 4);
+                    if (s == 2)
+                        store_factors(next, b + 2);
+                } else if constexpr (s == 0) {
+                    if (b & 2)
+                        store_factors(next, b + 2);
+                    else
+                        next = load_factors(b + 4);
+                }
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -804,17 +835,15 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
                 d[n & 3] = mfma<TERN>(a, x[j]);
                 if (i == FN - 1)
                     read_x(T, j);
-                if (G && j == LAG)
-                    gs[i & 1] = gnew;
                 const int m = n >= LAG ? n - LAG : n - LAG + FN * FM;
-                scale_add(m, n >= LAG ? f : fp);
+                scale_add(m, n >= LAG ? f : fp, n < LAG);
                 if (j == 1 && i < LATE)
-                    issue(T, min(b + 1, nb - 1), EARLY + i);
+                    issue(L, min(b + NS - 1, nb - 1), EARLY + i);
                 if (i >= FN - 2)
 #pragma unroll
                     for (int q = 0; q < NP; ++q)
                         if (q < EARLY && q % (2 * FM) == (i - (FN - 2)) * FM + j)
-                            issue(S, min(b + 2, nb - 1), q);
+                            issue(S, min(b + NS, nb - 1), q);
                 asm volatile("" : "+v"(acc[m / FM][m % FM]));  // (the same, down)
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -825,18 +854,25 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
         }
     };
 
-    load_factors(0);
-    store_factors(0);
-    // Every step loads the stage of the step after the next; the last ones load the
-    // last step again, into a stage that is not read (a branch there, or a second exit of the loop, had
+    // Every step loads a stage for NS steps on; the last ones load the last step
+    // again, into a stage that is not read (a branch there, or a second exit of the loop, had
     // the compiler copy the step).
+    auto fill = [&](auto S, int count) {
+        constexpr int s = decltype(S)::value;
 #pragma unroll
-    for (int q = 0; q < NP; ++q)
-        issue(std::integral_constant<int, 0>(), 0, q);
-    meet();
-#pragma unroll
-    for (int q = 0; q < EARLY; ++q)
-        issue(std::integral_constant<int, 1>(), min(1, nb - 1), q);
+        for (int q = 0; q < NP; ++q)
+            if (q < count)
+                issue(S, min(s, nb - 1), q);
+    };
+    fill(std::integral_constant<int, 0>(), NP);
+    if constexpr (NS == 4) {
+        fill(std::integral_constant<int, 1>(), NP);
+        fill(std::integral_constant<int, 2>(), NP);
+    }
+    next = load_factors(0);
+    store_factors(next, 0);
+    meet<(NS - 2) * NP>();
+    fill(std::integral_constant<int, NS - 1>(), EARLY);
     read_w(std::integral_constant<int, 0>(), 0);
     read_w(std::integral_constant<int, 0>(), 1);
     read_f(0);
@@ -846,18 +882,30 @@ __global__ void __launch_bounds__(C::THREADS, 2) tile_kernel(const Fp8Product p)
         f[j] = 0.f;
     }
     d[2] = d[3] = zero;
-    gs[1] = zero;
+    gs = 0.f;
+    if constexpr (!G)
+        gn = 0.f;
     int b = 0;
-    for (; b + 1 < nb; b += 2) {
+    for (; b + NS <= nb; b += NS) {
         step(std::integral_constant<int, 0>(), b);
         step(std::integral_constant<int, 1>(), b + 1);
+        if constexpr (NS == 4) {
+            step(std::integral_constant<int, 2>(), b + 2);
+            step(std::integral_constant<int, 3>(), b + 3);
+        }
     }
     if (b < nb)
         step(std::integral_constant<int, 0>(), b);
+    if constexpr (NS == 4) {
+        if (b + 1 < nb)
+            step(std::integral_constant<int, 1>(), b + 1);
+        if (b + 2 < nb)
+            step(std::integral_constant<int, 2>(), b + 2);
+    }
 #pragma unroll
     for (int n = FN * FM - LAG; n < FN * FM; ++n)
-        scale_add(n, f);
-    meet();  // no load into LDS outlives the workgroup
+        scale_add(n, f, false);
+    meet<0>();  // no load into LDS outlives the workgroup
 
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
@@ -929,25 +977,34 @@ hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
     const int64_t cus = device_cus(), m64 = (p.M + 63) / 64, m128 = (p.M + 127) / 128, m256 = (p.M + 255) / 256;
     const int64_t n128 = ((int64_t)p.N + 127) / 128, n256 = ((int64_t)p.N + 255) / 256, frags = m64 * ((p.N + 15) / 16);
     const double t_thin = 1.0 + p.nb * (frags <= cus ? 0.178 : 0.237 * rounds_of((frags + 1) / 2, cus));
-    const double t_64 = p.nb * (m64 * n128 <= cus ? 0.5 : 0.85 * rounds_of(m64 * n128, 2 * cus));
+    const double t_64 = p.nb * (m64 * n128 <= cus ? 0.48 : 0.85 * rounds_of(m64 * n128, 2 * cus));
     const double t_128 = p.nb * (m128 * n128 <= cus ? 0.72 : 1.2 * rounds_of(m128 * n128, 2 * cus));
     const double t_256 = p.nb * 1.75 * rounds_of(m256 * n256, cus);
     if (t_thin <= t_64 && t_thin <= t_128 && t_thin <= t_256)
         return launch_thin<false, 4>(p, m64, stream);
-    if (t_64 <= t_128 && t_64 <= t_256)
-        return launch_tiles<false, Tile<128, 64, 2, 2>>(p, m64, stream);
+    if (t_64 <= t_128 && t_64 <= t_256) {
+        // Four stages take so much LDS that a compute unit holds one workgroup: for one round.
+        // 64 rows of 18944 x 4096: 18.1 us, with two stages 23.7; 512 rows of 4096 x 4096 17.2 and 21.6.
+        return m64 * n128 <= cus ? launch_tiles<false, Tile<128, 64, 2, 2, 4>>(p, m64, stream)
+                                 : launch_tiles<false, Tile<128, 64, 2, 2>>(p, m64, stream);
+    }
     if (t_128 <= t_256)
         return launch_tiles<false, Tile<128, 128, 2, 2>>(p, m128, stream);
     return launch_tiles<false, Tile<256, 256, 2, 4>>(p, m256, stream);
 }
 
+// Few places an expert: streamed, K shared by eight waves; else tiles of 64
+// places.  64 experts, 8 a token, us, streamed and tiles: 2048 x 4096 at 1 token 9.0 and
+// 20, 16 tokens 37 and 47, 64 47 and 48, 128 62 and 48; 4096 x 1024 (scales per 128) at 16
+// 23 and 28, 128 36 and 38, 256 56 and 41.  Four stages took 193 instead of 171 us at
+// 2047 tokens of 4096 x 1024 (fewer workgroups a compute unit), tiles of 128 places 155,
+// but 207 instead of 200 of 2048 x 4096 and 59 instead of 41 at 256 tokens: an expert's last
+// tile is half empty on average.
 hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream)
 {
-    if (p.M <= 16 * p.E)
+    if (p.M <= (p.nb >= 16 ? 8 : 16) * (int64_t)p.E)
         return launch_thin<true, 1>(p, expert_tiles(p, 16), stream);
-    if (p.M <= 32 * p.E)
-        return launch_thin<true, 2>(p, expert_tiles(p, 32), stream);
-    return launch_tiles<true, Tile<128, 128, 2, 2>>(p, expert_tiles(p, 128), stream);
+    return launch_tiles<true, Tile<128, 64, 2, 2>>(p, expert_tiles(p, 64), stream);
 }
 
 }  // namespace ternary
