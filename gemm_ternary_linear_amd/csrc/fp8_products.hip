@@ -19,16 +19,65 @@ namespace ternary {
 
 namespace {
 
+// Whether outputs of a type take their sums from 16-bit operands.  The matrix unit
+// aligns the products of 32 8-bit (or fp4) factors to the largest before it adds them and
+// cuts what falls below: sums of a block were up to 2^-15.5 of the sum of magnitudes off
+// (random values over a few powers of two).  Rounding to bf16 or fp16 hides that; for fp32
+// outputs the factors become fp16 (exactly), whose products are added in full.
+constexpr bool wide_sums(int dtype) { return dtype == TERNARY_FP32; }
+
+// Eight e4m3 values (two registers), or eight fp4 values (one), as fp16.
+template <class A>
+__device__ __forceinline__ f16x8_t join_halves(A a, A b, A c, A d)
+{
+    return __builtin_bit_cast(f16x8_t, u32x4_v{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
+                                              __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d)});
+}
+__device__ __forceinline__ f16x8_t widen_fp8(int lo, int hi)
+{
+    return join_halves(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false),
+                       __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, true),
+                       __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, false),
+                       __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.f, true));
+}
+__device__ __forceinline__ f16x8_t widen_fp4(int v)
+{
+    return join_halves(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)v, 1.f, 0),
+                       __builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)v, 1.f, 1),
+                       __builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)v, 1.f, 2),
+                       __builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)v, 1.f, 3));
+}
+
 // One block of 128: 16 channels by 16 rows.  Without the instruction's own block
 // scales (both arguments 0) it issues faster: in a loop with the scaling of its results,
 // 4480 against 3883 TFLOP/s.  So an fp4 operand's +-2 stay, and half of each is left to
-// the channel's scale.
-template <bool TERN>
+// the channel's scale.  WIDE: by four 16-bit instructions of 32 each; what a lane holds of
+// w and x must be of the same k then.
+template <bool TERN, bool WIDE>
 __device__ __forceinline__ f32x4_t mfma(i32x8_v w, i32x8_v x)
 {
-    const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, zero, TERN ? 4 : 0, 0, 0, 0, 0, 0);
+    f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(TERN ? widen_fp4(w[q]) : widen_fp8(w[2 * q], w[2 * q + 1]),
+                                                       widen_fp8(x[2 * q], x[2 * q + 1]), d, 0, 0, 0);
+        return d;
+    } else {
+        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, d, TERN ? 4 : 0, 0, 0, 0, 0, 0);
+    }
 }
+// Chunks of 16 of a block of x that lane group g holds: the first, and how many on
+// the second lies.  8-bit weights: as the same chunks of w; ternary ones: as the
+// instruction pairs them with the fp4 operand's lane groups, which hold the codes 0, 64, 32
+// and 96 (and 31 more), or (WIDE) those codes' own.
+template <bool TERN, bool WIDE>
+__device__ __forceinline__ int first_chunk(int g)
+{
+    return !TERN ? g : WIDE ? (g & 1) * 4 + (g & 2) : g + (g & 2);
+}
+constexpr int second_chunk(bool tern, bool wide) { return !tern ? 4 : wide ? 1 : 2; }
+
 // Scale of a channel's fp4 products.
 __device__ __forceinline__ float channel_scale(uint16_t s) { return 0.5f * f16_bits_to_f32(s); }
 
@@ -257,7 +306,7 @@ __device__ __forceinline__ void load_group_scales(const uint16_t *row, int b0, i
 }
 
 // TERN: ternary weights of experts (G: with group scales).
-template <bool TERN, bool G, int MT, int FN>
+template <bool TERN, bool G, bool WIDE, int MT, int FN>
 __global__ void __launch_bounds__(kThreads, FN * MT <= 8 ? 4 : 2) thin_kernel(const Fp8Product p, int ks)
 {
     constexpr int U = thin_chunk(MT);
@@ -327,10 +376,8 @@ __global__ void __launch_bounds__(kThreads, FN * MT <= 8 ? 4 : 2) thin_kernel(co
 #pragma unroll
     for (int j = 0; j < MT; ++j)
         sp[j] = p.x_scale + x_row(16 * j + col) * nb;
-    // Chunks of a row that lane group g holds: g and g + 4, or for ternary
-    // weights (see below) those of 0, 1, 4, 5 and two further on.
-    const int cg = TERN ? g + (g & 2) : g;
-    const int c0 = cg ^ (col & 7), c1 = (cg + (TERN ? 2 : 4)) ^ (col & 7);
+    const int cg = first_chunk<TERN, WIDE>(g);
+    const int c0 = cg ^ (col & 7), c1 = (cg + second_chunk(TERN, WIDE)) ^ (col & 7);
     lds_u4 *const lx = (lds_u4 *)sx + wave * (U * MT * 128);
     const int xa = (col >> 3) * 64 + (col & 7) * 8;
     constant_float *wsp[FN];  // w's scales of each fragment (16 channels are in one block)
@@ -429,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, FN * MT <= 8 ? 4 : 2) thin_kernel(co
                 const i32x8_v xv = TERN ? odd_even(x0, x1) : join(x0, x1);
 #pragma unroll
                 for (int i = 0; i < FN; ++i) {
-                    const f32x4_t d = mfma<TERN>(a[i][u & 1], xv);
+                    const f32x4_t d = mfma<TERN, WIDE>(a[i][u & 1], xv);
                     const float f = TERN ? xs[j][u] : xs[j][u] * ws[i][u];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
@@ -470,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, FN * MT <= 8 ? 4 : 2) thin_kernel(co
 
 // ks: ways to share K.  Each wave should have a chunk of its own, and the more
 // channels a workgroup holds the fewer there are, so no more ways than chunks.
-template <bool TERN, bool G, int MT, int FN>
+template <bool TERN, bool G, bool WIDE, int MT, int FN>
 hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 {
     constexpr int U = thin_chunk(MT);
@@ -479,7 +526,7 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
     const int64_t wgs = tiles * ((p.N + 16 * FN * (kWaves / ks) - 1) / (16 * FN * (kWaves / ks)));
     if (wgs > INT32_MAX)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((thin_kernel<TERN, G, MT, FN>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, p, ks);
+    hipLaunchKernelGGL((thin_kernel<TERN, G, WIDE, MT, FN>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, p, ks);
     return hipGetLastError();
 }
 
@@ -502,22 +549,22 @@ inline int thin_fragments(int64_t frags, int most)
     return best;
 }
 
-template <bool TERN, bool G, int MT>
+template <bool TERN, bool G, bool WIDE, int MT>
 hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 {
     const int64_t frags = (p.N + 15) / 16 * tiles;
     if constexpr (TERN) {
-        return frags < 1024 ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
-                            : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
-    } else if constexpr (MT == 1 || MT == 4) {
-        return frags <= device_cus() ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
-                                     : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
+        return frags < 1024 ? launch_thin<TERN, G, WIDE, MT, 1>(p, tiles, stream)
+                            : launch_thin<TERN, G, WIDE, MT, 2>(p, tiles, stream);
+    } else if constexpr (WIDE || MT == 1 || MT == 4) {
+        return frags <= device_cus() ? launch_thin<TERN, G, WIDE, MT, 1>(p, tiles, stream)
+                                     : launch_thin<TERN, G, WIDE, MT, 2>(p, tiles, stream);
     } else {
         switch (thin_fragments(frags, 5)) {
-        case 1: return launch_thin<TERN, G, MT, 1>(p, tiles, stream);
-        case 2: return launch_thin<TERN, G, MT, 2>(p, tiles, stream);
-        case 3: return launch_thin<TERN, G, MT, 3>(p, tiles, stream);
-        default: return launch_thin<TERN, G, MT, 5>(p, tiles, stream);
+        case 1: return launch_thin<TERN, G, WIDE, MT, 1>(p, tiles, stream);
+        case 2: return launch_thin<TERN, G, WIDE, MT, 2>(p, tiles, stream);
+        case 3: return launch_thin<TERN, G, WIDE, MT, 3>(p, tiles, stream);
+        default: return launch_thin<TERN, G, WIDE, MT, 5>(p, tiles, stream);
         }
     }
 }
@@ -526,10 +573,15 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 template <bool TERN, int MT>
 hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 {
-    if constexpr (TERN)
-        return p.group ? launch_thin<true, true, MT>(p, tiles, stream) : launch_thin<true, false, MT>(p, tiles, stream);
-    else
-        return launch_thin<false, false, MT>(p, tiles, stream);
+    auto run = [&](auto wide) {
+        constexpr bool W = decltype(wide)::value;
+        if constexpr (TERN)
+            return p.group ? launch_thin<true, true, W, MT>(p, tiles, stream)
+                           : launch_thin<true, false, W, MT>(p, tiles, stream);
+        else
+            return launch_thin<false, false, W, MT>(p, tiles, stream);
+    };
+    return wide_sums(p.dtype) ? run(std::true_type()) : run(std::false_type());
 }
 
 // ---------------------------------------------------------------- many rows
@@ -556,6 +608,7 @@ __device__ __forceinline__ f32x4_t load_scales_uniform(const float *row, int b0,
 template <bool TERN, bool G, int DT, class C>
 __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Product p)
 {
+    constexpr bool WIDE = wide_sums(DT);
     constexpr int TN = C::TN, TM = C::TM, FN = C::FN, FM = C::FM, THREADS = C::THREADS, NS = C::NS;
     constexpr int XI = TM * 8 / THREADS;                      // x loads of a thread and stage
     constexpr int WCH = TERN ? TN * 2 : TN * 8;               // 16-byte chunks of w in a stage
@@ -719,14 +772,13 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
         for (int j = 0; j < FM; ++j)
             acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
-    // Chunks of a row that lane group g holds: g and g + 4.  Ternary: the codes of
-    // two fragments come by one load, 16 bytes of the first fragment's in lanes 0 .. 31, of the
-    // second's in the others; exchanging the halves of each (permlane32_swap)
-    // leaves a fragment with the codes 0, 64, 32 and 96 (and 31 more) in its lane
-    // groups, so x's chunks are 0, 1, 4, 5 and those two further on.
+    // Ternary: the codes of two fragments come by one load, 16 bytes of the first
+    // fragment's in lanes 0 .. 31, of the second's in the others; exchanging the halves of
+    // each (permlane32_swap) leaves a fragment with the codes 0, 64, 32 and 96 (and 31 more)
+    // in its lane groups.
     static_assert(!TERN || FN % 2 == 0);
-    const int xa = (wm * FM * 16 + col) * 8, cg = TERN ? g + (g & 2) : g;
-    const int c0 = cg ^ swz(col), c1 = (cg + (TERN ? 2 : 4)) ^ swz(col);
+    const int xa = (wm * FM * 16 + col) * 8, cg = first_chunk<TERN, WIDE>(g);
+    const int c0 = cg ^ swz(col), c1 = (cg + second_chunk(TERN, WIDE)) ^ swz(col);
     const int wa = TERN ? wn * FN * 32 + lane : (wn * FN * 16 + col) * 8;
 
     // Operands on their way from LDS: w's two fragments ahead (ternary: two
@@ -832,7 +884,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
                 if (i == 0)
                     x[j] = TERN ? odd_even(rx[j][0], rx[j][1]) : join(rx[j][0], rx[j][1]);
                 asm volatile("" : "+v"(x[j]));  // (nothing: keeps the instruction from moving up)
-                d[n & 3] = mfma<TERN>(a, x[j]);
+                d[n & 3] = mfma<TERN, WIDE>(a, x[j]);
                 if (i == FN - 1)
                     read_x(T, j);
                 const int m = n >= LAG ? n - LAG : n - LAG + FN * FM;
@@ -932,7 +984,7 @@ hipError_t launch_tiles(const Fp8Product &p, int64_t tiles, hipStream_t stream)
     if (wgs > INT32_MAX)
         return hipErrorInvalidValue;
     with_dtype(p.dtype, [&](auto dt) {
-        constexpr int DT = decltype(dt)::value;
+        constexpr int DT = wide_sums(decltype(dt)::value) && C::FN * C::FM > 16 ? TERNARY_BF16 : decltype(dt)::value;
         if (TERN && p.group)
             hipLaunchKernelGGL((tile_kernel<TERN, TERN, DT, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
         else
@@ -980,15 +1032,15 @@ hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
     const double t_64 = p.nb * (m64 * n128 <= cus ? 0.48 : 0.85 * rounds_of(m64 * n128, 2 * cus));
     const double t_128 = p.nb * (m128 * n128 <= cus ? 0.72 : 1.2 * rounds_of(m128 * n128, 2 * cus));
     const double t_256 = p.nb * 1.75 * rounds_of(m256 * n256, cus);
-    if (t_thin <= t_64 && t_thin <= t_128 && t_thin <= t_256)
+    if (t_thin <= t_64 && t_thin <= t_128 && (t_thin <= t_256 || wide_sums(p.dtype)))
         return launch_thin<false, 4>(p, m64, stream);
-    if (t_64 <= t_128 && t_64 <= t_256) {
+    if (t_64 <= t_128 && (t_64 <= t_256 || wide_sums(p.dtype))) {
         // Four stages take so much LDS that a compute unit holds one workgroup: for one round.
         // 64 rows of 18944 x 4096: 18.1 us, with two stages 23.7; 512 rows of 4096 x 4096 17.2 and 21.6.
         return m64 * n128 <= cus ? launch_tiles<false, Tile<128, 64, 2, 2, 4>>(p, m64, stream)
                                  : launch_tiles<false, Tile<128, 64, 2, 2>>(p, m64, stream);
     }
-    if (t_128 <= t_256)
+    if (t_128 <= t_256 || wide_sums(p.dtype))  // (16-bit operands leave no registers for larger tiles)
         return launch_tiles<false, Tile<128, 128, 2, 2>>(p, m128, stream);
     return launch_tiles<false, Tile<256, 256, 2, 4>>(p, m256, stream);
 }
