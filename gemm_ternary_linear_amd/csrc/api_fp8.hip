@@ -25,6 +25,9 @@ int64_t elem_bytes(int dtype)
     return dtype == TERNARY_BF16 || dtype == TERNARY_FP16 ? 2 : dtype == TERNARY_FP32 ? 4 : 0;
 }
 
+// Most places of the experts' products: a tile past the last stays inside 32 bits.
+constexpr int64_t kMaxPlaces = (int64_t)1 << 30;
+
 bool dim_ok(int64_t n, int64_t lo, int64_t hi = kMaxDim) { return n >= lo && n <= hi; }
 
 }  // namespace
@@ -151,7 +154,7 @@ int ternary_linear_experts(const uint8_t *x, const float *x_scale, int64_t x_row
     const bool tokens = rows == TERNARY_ROWS_TOKENS;
     if ((!tokens && rows != TERNARY_ROWS_SORTED) || !dim_ok(E, 1, TERNARY_MAX_EXPERTS) ||
         !dim_ok(N, 0) || !dim_ok(K, 1, kMaxProductK) || K % 4 ||
-        (group_size > 0 && K % group_size) || !dim_ok(R, 0, INT32_MAX) ||
+        (group_size > 0 && K % group_size) || !dim_ok(R, 0, kMaxPlaces) ||
         !dim_ok(x_rows, R ? 1 : 0, INT32_MAX) || (!tokens && x_rows < R) ||
         (tokens && !dim_ok(top_k, 1, TERNARY_MAX_TOP_K)))
         return TERNARY_ERR_SHAPE;

@@ -110,8 +110,8 @@ __device__ __forceinline__ bool find_tile_of(const int32_t *offsets, int E, int 
     int mine = 0;
 #pragma unroll
     for (int i = 0; i < EP; ++i) {
-        const int n = min(o[i + 1], R) - max(o[i], 0);
-        mine += n > 0 ? (n + BM - 1) / BM : 0;
+        const int a = max(o[i], 0), b = min(o[i + 1], R);
+        mine += b > a ? (b - a + BM - 1) / BM : 0;
     }
     const int incl = wave_scan(mine);
     int left = idx - (incl - mine), fe = -1, f0 = 0, f1 = 0;

@@ -3,9 +3,9 @@
 // Per block of 128 values (of one row, or of 128 rows): s = max|v| / 448 in
 // fp32, q = v / s rounded to fp32, then to the nearest e4m3 (the hardware
 // conversion, ties to even).  The codes are rounded against the stored s, as
-// ternary_quantize rounds against its stored scale; the quotient is a real
-// fp32 division, because a product with a rounded 1/s would move values off
-// the ties that a 16-bit v often hits exactly.  v is x, or for SwiGLU
+// ternary_quantize rounds against its stored scale; the quotient is the rounded
+// one, because a product with a rounded 1/s would move values off the ties that a
+// 16-bit v often hits exactly.  v is x, or for SwiGLU
 // silu(gate) * up in fp32.
 //
 // HBM-bound: e bytes read (2 e for SwiGLU) and one written per value.  A row
@@ -25,18 +25,37 @@ constexpr int kThreads = 256;
 __device__ __forceinline__ u32x2_v codes8(const float v[8], float s)
 {
     float r[8];
+    // The rounded quotient: by one reciprocal (corrected once) and, for each value, a
+    // product whose exact remainder corrects it.  Three operations a value where a division takes
+    // ten; remainders stay exact while s is neither tiny nor huge.
+    const bool mid = s > 0x1p-100f && s < 0x1p100f;
+    if (__builtin_amdgcn_ballot_w64(!mid) == 0) {
+        const float a = __builtin_amdgcn_rcpf(s), inv = fmaf(fmaf(-s, a, 1.f), a, a);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float d = s > 0.f ? v[i] / s : (v[i] != v[i] ? v[i] : 0.f);
-        // a subnormal s can leave a quotient above 448: the largest code then
-        // (NaN passes the comparisons and stays NaN)
-        r[i] = d > kE4m3Max ? kE4m3Max : (d < -kE4m3Max ? -kE4m3Max : d);
+        for (int i = 0; i < 8; ++i) {
+            const float q = v[i] * inv;
+            r[i] = fmaf(fmaf(-s, q, v[i]), inv, q);  // (at most 448)
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = s > 0.f ? v[i] / s : (v[i] != v[i] ? v[i] : 0.f);
+            // a subnormal s can leave a quotient above 448: the largest code then
+            // (NaN passes the comparisons and stays NaN)
+            r[i] = d > kE4m3Max ? kE4m3Max : (d < -kE4m3Max ? -kE4m3Max : d);
+        }
     }
     int a = __builtin_amdgcn_cvt_pk_fp8_f32(r[0], r[1], 0, false);
     a = __builtin_amdgcn_cvt_pk_fp8_f32(r[2], r[3], a, true);
     int b = __builtin_amdgcn_cvt_pk_fp8_f32(r[4], r[5], 0, false);
     b = __builtin_amdgcn_cvt_pk_fp8_f32(r[6], r[7], b, true);
     return u32x2_v{(uint32_t)a, (uint32_t)b};
+}
+
+// silu(g) * u.  The reciprocal's last bit is lost beside exp's.
+__device__ __forceinline__ float swiglu(float g, float u)
+{
+    return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)) * u;
 }
 
 // Values k .. k+7 of a row (columns from K on are zeros).  VEC: 16-byte loads
@@ -56,7 +75,7 @@ __device__ __forceinline__ void values8(const void *x, int64_t row, int K, int k
             load8<DT>(x, row + K + k, u);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = v[i] / (1.f + __expf(-v[i])) * u[i];
+                v[i] = swiglu(v[i], u[i]);
         }
     } else {
 #pragma unroll
@@ -65,7 +84,7 @@ __device__ __forceinline__ void values8(const void *x, int64_t row, int K, int k
             if (k + i < K) {
                 v[i] = load_elem<DT>(x, row + k + i);
                 if constexpr (SWIGLU)
-                    v[i] = v[i] / (1.f + __expf(-v[i])) * load_elem<DT>(x, row + K + k + i);
+                    v[i] = swiglu(v[i], load_elem<DT>(x, row + K + k + i));
             }
         }
     }
@@ -93,7 +112,8 @@ __global__ void __launch_bounds__(kThreads)
     const int l = threadIdx.x & 15;
     for (int64_t u = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4); u < blocks;
          u += stride) {
-        const int64_t row = u / kb;
+        // (a 64-bit division would cost as much as the block's arithmetic)
+        const int64_t row = blocks <= UINT32_MAX ? (int64_t)((uint32_t)u / (uint32_t)kb) : u / kb;
         const int k = (int)(u - row * kb) * kFp8Block + 8 * l;
         float v[8];
         values8<DT, SWIGLU, VEC>(x, row * ldx, K, k, v);

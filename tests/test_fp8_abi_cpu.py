@@ -88,7 +88,7 @@ def experts(tl, x=F, xs=2 * F, n=8, t=3 * F, s=4 * F, E=4, N=256, K=256, g=-1, o
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=3), DTYPE), (dict(g=64), GROUP), (dict(g=32), GROUP), (dict(g=0), GROUP), (dict(K=130), SHAPE), (dict(K=0), SHAPE),
     (dict(K=384, g=256), SHAPE), (dict(K=260, g=128), SHAPE), (dict(E=0), SHAPE), (dict(E=513), SHAPE), (dict(N=-1), SHAPE),
-    (dict(R=-1), SHAPE), (dict(R=1 << 31), SHAPE), (dict(n=0), SHAPE), (dict(rows=2), SHAPE), (dict(rows=1, n=15), SHAPE),
+    (dict(R=-1), SHAPE), (dict(R=(1 << 30) + 1), SHAPE), (dict(n=0), SHAPE), (dict(rows=2), SHAPE), (dict(rows=1, n=15), SHAPE),
     (dict(k=0), SHAPE), (dict(k=33), SHAPE), (dict(x=0), NULL), (dict(xs=0), NULL), (dict(t=0), NULL), (dict(s=0), NULL),
     (dict(off=0), NULL), (dict(order=0), NULL), (dict(y=0), NULL), (dict(x=F + 8), ALIGN), (dict(t=3 * F + 8), ALIGN),
     (dict(s=4 * F + 1), ALIGN), (dict(off=5 * F + 2), ALIGN), (dict(order=6 * F + 1), ALIGN), (dict(y=7 * F + 8), ALIGN),

@@ -178,6 +178,33 @@ def test_experts(tl, T, E, k, N, K, g, dtype):
     assert torch.equal(got, tl.linear_experts(*args, dtype=DT[dtype])), "the same inputs give the same bits"
 
 
+@pytest.mark.parametrize("T", [4, 500])
+def test_experts_foreign_indices(tl, T):
+    """Offsets and order that do not describe a routing: nothing outside the arguments is read or written, and the
+    rows that they leave out stay as they were."""
+    say(f"experts foreign indices T={T}")
+    rng = np.random.default_rng(T)
+    E, k, N, K = 5, 2, 48, 256
+    xq, xs = ref.codes_of(rng, T, K), ref.scales_of(rng, T, K // 128)
+    codes = torch.stack([torch.from_numpy(ref.tile_codes(rng.integers(-1, 2, (N, K)).astype(np.int8))) for _ in range(E)]).cuda()
+    s = ref.dev(ref.scales_of(rng, E, N).astype(np.float16))
+    R = T * k
+    r = routing(tl, draw_ids(rng, T, E, k, 0, 0), np.zeros((T, k), np.float32), E)
+    for off in ([0, R, -7, R + 100, 3, 2 ** 31 - 1], [-2 ** 31, -5, -1, 0, 0, 0], [5, 4, 3, 2, 1, 0], [R] * 6):
+        order = torch.full((R,), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+        order[::2] = -2 ** 31
+        bad = r._replace(offsets=torch.tensor(off, dtype=torch.int32, device="cuda"), order=order)
+        buf = torch.full((R * N + 64,), 77.0, device="cuda")
+        tl.linear_experts(ref.fp8_dev(xq), ref.dev(xs), codes, s, bad, out=buf[32:32 + R * N].view(R, N))
+        torch.cuda.synchronize()
+        assert bool((buf[:32] == 77).all()) and bool((buf[32 + R * N:] == 77).all())
+        if max(off) <= 0 or off[0] >= R:
+            assert bool((buf == 77).all())
+    bad = r._replace(slots=torch.where(r.slots % 3 == 0, torch.full_like(r.slots, 2 ** 31 - 1), torch.full_like(r.slots, -9)))
+    y = torch.full((R, 40), torch.nan, device="cuda")
+    assert bool((tl.combine(y, bad) == 0).all())
+
+
 @pytest.mark.parametrize("T", [3, 90, 700])
 def test_experts_rows_apart(tl, T):
     """A NaN in one token's x shows in that token's rows only; a NaN scale of an expert in that channel only."""

@@ -160,6 +160,21 @@ def test_linear(tl, M, N, K, dtype):
     assert torch.equal(got, run_linear(tl, xq, xs, wq, ws, DT[dtype])), "the same inputs give the same bits"
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 128, 512), (20, 200, 512), (60, 130, 256), (200, 256, 512), (700, 300, 256)])
+def test_linear_fp32_sums(tl, M, N, K):
+    """fp32 outputs of factors over many powers of two: a block's sum takes four instructions of 32 products, each
+    off by at most 2^-23 of their magnitudes, then a scaling, the scales' product and a sum: (4 + 2 nb + 4) of
+    those in all. (Sums from 8-bit operands would be up to 2^-15.5 off.)"""
+    say(f"linear fp32 sums {M} {N} {K}")
+    rng = np.random.default_rng(M + N)
+    spread = lambda *s: rng.standard_normal(s) * np.exp(1.5 * rng.standard_normal(s))  # noqa: E731
+    xq, xs = ref.quantize(spread(M, K).astype(np.float32), False)
+    wq, ws = ref.quantize(spread(N, K).astype(np.float32), True)
+    xw, ww = ref.wide(xq, xs), ref.wide(wq, ws, 128)
+    got = run_linear(tl, xq, xs, wq, ws, torch.float32).double().cpu().numpy()
+    assert np.all(np.abs(got - xw @ ww.T) <= (4 + 2 * (K // 128) + 4) * 2.0 ** -23 * (np.abs(xw) @ np.abs(ww).T))
+
+
 @pytest.mark.parametrize("M", [1, 20, 150, 600])
 def test_linear_nan(tl, M):
     """A NaN code or scale shows in the outputs that read it, and in no other."""
