@@ -54,16 +54,17 @@ __device__ __forceinline__ u32x2_v codes8(const float v[8], float s)
 
 // silu(g) * u, silu within about two roundings: exp(-g) as a power of two whose
 // argument's rounding (up to |g| 2^-24 of the result) is put back, and a quotient by a
-// corrected reciprocal.  From 2^100 on exp(-g) is taken as it comes (infinity: silu is 0).
+// corrected reciprocal.  From 2^100 on, and below 2^-100, exp(-g) is taken as it comes
+// (infinity: silu is 0; 0: silu is g): there t or the remainder may be infinite.
 __device__ __forceinline__ float swiglu(float g, float u)
 {
     const float hi = 0x1.715476p+0f, lo = 0x1.4ae0cp-26f;  // log2(e), and what fp32 leaves of it
     const float t = -g * hi, rest = fmaf(-g, hi, -t) - g * lo;
     const float e = __builtin_amdgcn_exp2f(t);
-    const bool big = t > 100.f;
-    const float d = 1.f + (big ? e : fmaf(e, rest * 0x1.62e43p-1f, e));
+    const bool far = fabsf(t) > 100.f;
+    const float d = 1.f + (far ? e : fmaf(e, rest * 0x1.62e43p-1f, e));
     const float r = __builtin_amdgcn_rcpf(d), q = g * r;
-    return (big ? q : fmaf(fmaf(-d, q, g), r, q)) * u;
+    return (far ? q : fmaf(fmaf(-d, q, g), r, q)) * u;
 }
 
 // Values k .. k+7 of a row (columns from K on are zeros).  VEC: 16-byte loads

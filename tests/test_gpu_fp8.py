@@ -115,6 +115,29 @@ def test_quantize_swiglu(tl, M, K, dtype):
     assert not host(q)[:, K:].any()
 
 
+@pytest.mark.parametrize("vec", [True, False])
+def test_quantize_swiglu_far_gates(tl, vec):
+    """Gates whose exponential, or its argument, leaves fp32: silu is g above and 0 below."""
+    say(f"swiglu far gates {vec}")
+    K = 128 if vec else 127
+    gates = [3.4e38, 2.4e38, 2.3e38, 1e30, 200., 100., 69.4, 69.2, 1.5, -69.2, -69.4, -100., -200., -3e38]
+    g = torch.tensor(gates, dtype=torch.float32)[:, None].expand(-1, K)
+    u = (torch.tensor([1. / max(abs(v), 1.) for v in gates]).float())[:, None].expand(-1, K)
+    q, s = tl.fp8_quantize(torch.cat([g, u], 1).contiguous().cuda(), act="swiglu")
+    silu = g[:, 0].double() / (1 + torch.exp(-g[:, 0].double()))
+    # a row of one value is its scale times 448: four roundings of fp32, and 2^-149 where it underflows
+    want = (silu * u[:, 0].double()).abs()
+    got = s[:, 0].cpu().double() * 448
+    assert ((got - want).abs() <= want * 8 * 2.0 ** -24 + 448 * 2.0 ** -126).all(), (got, want)
+    x = torch.ones(2, 2 * K)
+    x[0, 5] = float("inf")
+    x[1, 5] = -float("inf")  # -inf / inf: NaN, left out of the block's largest
+    q, s = tl.fp8_quantize(x.cuda(), act="swiglu")
+    assert torch.isinf(s[0, 0]) and torch.isfinite(s[1, 0])
+    codes = q.cpu().view(torch.uint8) & 0x7f
+    assert codes[0, 5] == 0x7f and (codes[0, :5] == 0).all() and codes[1, 5] == 0x7f and (codes[1, :5] == 0x7e).all()
+
+
 def linear_case(rng, M, N, K, exact):
     if exact:
         return (ref.codes_of(rng, M, K), ref.scales_of(rng, M, K // 128), ref.codes_of(rng, N, K),
