@@ -2,7 +2,10 @@
 //     out[t, n] = add[t, n] + sum_j weights[t, j] * y[slots[t, j], n]
 // in fp32, j ascending, rounded once.  HBM-bound: every expert row is read
 // once and every output written once.  A lane takes 8 columns of a token (one
-// 16-byte load a row for 16-bit types), its k rows in flight together.
+// 16-byte load a row for 16-bit types).
+//
+// Measured (kernel trace, bf16): 2047 x 4096 of 8 rows a token 29.0 us for 151 MB (5.2
+// TB/s, part of it from cache between repeats); 1 x 4096 4.2 us, an empty launch 1.9.
 #include "fp8_common.h"
 #include "internal.h"
 

@@ -12,6 +12,9 @@
 // block is 16 lanes of 8 values (one 16-byte load each for 16-bit types), its
 // maximum a butterfly over those lanes, so a wave does four blocks at a time
 // with no LDS; a weight tile is a workgroup, eight rows a lane.
+//
+// Measured (kernel trace, bf16): 16384 x 1024 SwiGLU 18.5 us for 84 MB (4.5 TB/s, part of it
+// from cache between repeats; a copy of 2 GiB 4.9); 1 x 4096 2.1 us, an empty launch 1.9.
 #include "fp8_common.h"
 #include "internal.h"
 

@@ -18,6 +18,10 @@
 // (2 bytes per chunk and expert, from L2, 16 bytes a load).  Beyond kFlatTokens that sum would
 // grow with the square of the batch, so a kernel in between adds it up per
 // 1024 tokens.
+//
+// Measured (kernel traces): 1 token, 64 experts 3.9 us; 4096 tokens, 256 experts, 8 a token
+// 12.6 us to choose and 8.6 to place, where the logits' bytes would take 1.  Choosing is
+// bound by its chain of top_k maxima and by 64-bit arithmetic, not by memory.
 #include <cfloat>
 
 #include "fp8_common.h"
