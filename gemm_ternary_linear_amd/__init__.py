@@ -535,10 +535,12 @@ def route(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.
     offsets = torch.empty(E + 1, dtype=torch.int32, device=d)
     order = torch.empty(T * top_k, dtype=torch.int32, device=d)
     slots = torch.empty_like(ids)
-    ws = torch.empty(need, dtype=torch.uint8, device=d).data_ptr() if need else None
+    # (held until the launches are enqueued: freed before, another thread's call could get it between them)
+    ws = torch.empty(need, dtype=torch.uint8, device=d) if need else None
     _call("ternary_route", dev, logits.data_ptr(), dt, T, E, bias.data_ptr() if bias is not None else None,
           sc, groups, top_groups, top_k, 1 if renormalize else 0, scale, ids.data_ptr(),
-          weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), slots.data_ptr(), ws)
+          weights.data_ptr(), offsets.data_ptr(), order.data_ptr(), slots.data_ptr(),
+          ws.data_ptr() if need else None)
     return Routing(ids, weights, offsets, order, slots)
 
 

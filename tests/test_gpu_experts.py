@@ -1,5 +1,7 @@
 """route, linear_experts and combine against 64-bit references, and a whole mixture of experts."""
 
+import weakref
+
 import numpy as np
 import pytest
 import torch
@@ -93,6 +95,28 @@ def test_route_many_tokens(tl):
         off, order, slots = ref.sort_slots(ids.cpu().numpy(), E)
         for a, b in ((r.offsets, off), (r.order, order), (r.slots, slots)):
             assert np.array_equal(a.cpu().numpy(), b)
+
+
+def test_route_holds_its_workspace(tl, monkeypatch):
+    """The workspace lives until the kernels are enqueued: freed before, another thread could be given it between
+    them (the call lets other threads run)."""
+    say("route workspace")
+    made, alive, empty, call = [], [], torch.empty, tl._call
+
+    def recording(*a, **kw):
+        t = empty(*a, **kw)
+        if kw.get("dtype") == torch.uint8:
+            made.append(weakref.ref(t))
+        return t
+
+    def checked(name, *a):
+        alive.extend(r() is not None for r in made)
+        return call(name, *a)
+
+    monkeypatch.setattr(tl.torch, "empty", recording)
+    monkeypatch.setattr(tl, "_call", checked)
+    r = tl.route(torch.randn(200, 64, device="cuda"), 8)
+    assert alive == [True] and bool((r.ids >= 0).all())
 
 
 def routing(tl, ids, w, E):
