@@ -34,7 +34,7 @@ namespace {
 constexpr int kWaves = 16, kThreads = kWaves * 64;
 constexpr int kFusedTokens = 64;    // tokens one workgroup routes and sorts
 constexpr int kChunk = 16;          // tokens of a mask
-constexpr int kPlaceTokens = 64;    // tokens a workgroup places
+constexpr int kWideTokens = 4096;   // most tokens placed 16 a workgroup; beyond, 64
 constexpr int kSuper = 1024;        // tokens of a row of sums
 constexpr int kFlatTokens = 8192;   // most tokens without the rows of sums
 constexpr int kMaxE = TERNARY_MAX_EXPERTS, kMaxK = TERNARY_MAX_TOP_K;
@@ -354,10 +354,11 @@ __global__ void __launch_bounds__(256) route_sums_kernel(const RouteArgs a)
     }
 }
 
-// Places the slots of 64 tokens.
+// Places the slots of TOKENS tokens.
+template <int TOKENS>
 __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteArgs a, bool flat)
 {
-    constexpr int PER = kPlaceTokens / kChunk;
+    constexpr int PER = TOKENS / kChunk;
     __shared__ int total[kMaxE + 1], before[kMaxE];
     __shared__ uint64_t mask[kMaxE];
     const uint16_t *masks = static_cast<const uint16_t *>(a.workspace);
@@ -421,8 +422,8 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteArgs a
     if (blockIdx.x == 0)
         for (int i = tid; i <= E; i += kThreads)
             a.offsets[i] = total[i];
-    const int64_t s0 = (int64_t)blockIdx.x * kPlaceTokens * a.k, n = (int64_t)a.T * a.k;
-    for (int i = tid; i < kPlaceTokens * a.k && s0 + i < n; i += kThreads) {
+    const int64_t s0 = (int64_t)blockIdx.x * TOKENS * a.k, n = (int64_t)a.T * a.k;
+    for (int i = tid; i < TOKENS * a.k && s0 + i < n; i += kThreads) {
         const int64_t s = s0 + i;
         const int id = a.ids[s], t = i / a.k;
         int r = -1;
@@ -477,8 +478,14 @@ hipError_t launch_route(const RouteArgs &a, int dtype, hipStream_t stream)
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL(route_place_kernel, dim3((unsigned)((a.T + kPlaceTokens - 1) / kPlaceTokens)),
-                       dim3(kThreads), 0, stream, a, flat);
+    auto place = [&](auto kernel, int tokens) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)((a.T + tokens - 1) / tokens)), dim3(kThreads), 0, stream, a,
+                           flat);
+    };
+    if (a.T <= kWideTokens)
+        place(route_place_kernel<16>, 16);
+    else
+        place(route_place_kernel<64>, 64);
     return hipGetLastError();
 }
 
