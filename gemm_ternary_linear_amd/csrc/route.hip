@@ -348,8 +348,13 @@ __global__ void __launch_bounds__(256) route_sums_kernel(const RouteArgs a)
     const int64_t chunks = chunks_of(a.T), first = (int64_t)blockIdx.x * PER;
     for (int e = threadIdx.x; e < a.E; e += 256) {
         int s = 0;
-        for (int64_t c = first; c < first + PER && c < chunks; ++c)
-            s += __popc(masks[c * mask_row(a.E) + e]);
+        // (no early end: the loads of 16 steps go out together)
+#pragma unroll 16
+        for (int i = 0; i < PER; ++i) {
+            const int64_t c = first + i;
+            const int n = __popc(masks[min(c, chunks - 1) * mask_row(a.E) + e]);
+            s += c < chunks ? n : 0;
+        }
         sums[(int64_t)blockIdx.x * a.E + e] = s;
     }
 }
