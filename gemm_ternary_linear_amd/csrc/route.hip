@@ -14,14 +14,25 @@
 // the chunks' counts add up to the rest.  Up to kFusedTokens tokens one
 // workgroup routes and sorts (one launch); more are routed by a workgroup per
 // 16 tokens, whose masks go to the workspace, and placed by a second kernel, a
-// workgroup per 64 tokens, each adding up the masks of all chunks itself
+// workgroup per 16 or 64 tokens, each adding up the masks of all chunks itself
 // (2 bytes per chunk and expert, from L2, 16 bytes a load).  Beyond kFlatTokens that sum would
 // grow with the square of the batch, so a kernel in between adds it up per
 // 1024 tokens.
 //
-// Measured (kernel traces): 1 token, 64 experts 3.9 us; 4096 tokens, 256 experts, 8 a token
-// 12.6 us to choose and 8.6 to place, where the logits' bytes would take 1.  Choosing is
-// bound by its chain of top_k maxima and by 64-bit arithmetic, not by memory.
+// Limits, us a call in a graph, experts x top_k behind the tokens.  One launch against two:
+// 24 x 64 x 4 5.8 and 7.5, 24 x 256 x 8 12.9 and 12.5, 32 x 64 x 4 7.1 and 7.5, 32 x 256 x 8
+// 17.0 and 12.7, 48 x 64 x 4 9.1 and 7.5, 64 x 64 x 4 11.1 and 7.5, 64 x 256 x 8 29.9 and 12.7;
+// but called one after another from Python, where the second launch and its workspace weigh, 32 x
+// 64 x 4 12.9 and (33 tokens) 16.8, 32 x 256 x 8 16.9 and 17.0.  So one launch up to 64 tokens
+// of at most 64 experts, and up to 32 of more.  16 against 64 tokens placed a workgroup: 128 x 64 x 4 7.8 and 9.0,
+// 4096 x 256 x 8 18.1 and 18.9, 8192 x 256 x 8 31.0 and 27.7, 100000 x 256 x 8 431 and 244.  Rows of
+// sums against none: 8193 x 64 x 4 16.6 and 13.6, 8193 x 256 x 8 28.8 and 29.4, 12000 x 512 x 8
+// 53.5 and 59.5, 32000 x 64 x 4 28.4 and 31.9, 100000 x 256 x 8 232 and 534.
+//
+// What 4096 x 256 x 8 by sigmoid with groups spends (kernel traces, parts left out in
+// turn): 12.4 us to choose, of which 3.9 are seven of the eight rounds of maxima and 1.5 the
+// 64-bit sigmoid; placing 64 tokens a workgroup took 8.4, of which 2.6 were adding up masks.
+// Unrolling that sum further changed nothing.  The logits' bytes would take 1 us.
 #include <cfloat>
 
 #include "fp8_common.h"
@@ -32,7 +43,7 @@ namespace ternary {
 namespace {
 
 constexpr int kWaves = 16, kThreads = kWaves * 64;
-constexpr int kFusedTokens = 64;    // tokens one workgroup routes and sorts
+constexpr int kFusedTokens = 64;    // most tokens one workgroup routes and sorts
 constexpr int kChunk = 16;          // tokens of a mask
 constexpr int kWideTokens = 4096;   // most tokens placed 16 a workgroup; beyond, 64
 constexpr int kSuper = 1024;        // tokens of a row of sums
@@ -305,6 +316,9 @@ __global__ void __launch_bounds__(kThreads) route_few_kernel(const RouteArgs a)
     }
 }
 
+// Most tokens of one launch.
+inline int fused_tokens(int64_t E) { return E <= 64 ? kFusedTokens : kFusedTokens / 2; }
+
 __host__ __device__ inline int64_t chunks_of(int64_t T) { return (T + kChunk - 1) / kChunk; }
 // Masks lie in rows of whole 16 bytes; the rows of sums follow them.
 __host__ __device__ inline int mask_row(int64_t E) { return (int)((E + 7) & ~(int64_t)7); }
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(kThreads) route_place_kernel(const RouteArgs a
 
 int64_t route_workspace(int64_t T, int64_t E)
 {
-    if (T <= kFusedTokens)
+    if (T <= fused_tokens(E))
         return 0;
     return mask_bytes(T, E) + (T <= kFlatTokens ? 0 : (T + kSuper - 1) / kSuper * E * 4);
 }
@@ -458,7 +472,7 @@ hipError_t launch_route(const RouteArgs &a, int dtype, hipStream_t stream)
     with_dtype(dtype, [&](auto dt) {
         constexpr int DT = decltype(dt)::value;
         auto run = [&](auto few, auto many) {
-            if (a.T <= kFusedTokens)
+            if (a.T <= fused_tokens(a.E))
                 hipLaunchKernelGGL(few, dim3(1), dim3(kThreads), lds, stream, a);
             else
                 hipLaunchKernelGGL(many, dim3((unsigned)chunks_of(a.T)), dim3(kThreads), lds, stream, a);
@@ -473,7 +487,7 @@ hipError_t launch_route(const RouteArgs &a, int dtype, hipStream_t stream)
             run(route_few_kernel<DT, 8>, route_many_kernel<DT, 8>);
     });
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || a.T <= kFusedTokens)
+    if (e != hipSuccess || a.T <= fused_tokens(a.E))
         return e;
     const bool flat = a.T <= kFlatTokens;
     if (!flat) {

@@ -74,7 +74,8 @@ def test_route_refuses(tl, kw, status):
 
 def test_route_workspace(tl):
     L = tl.lib()
-    assert L.ternary_route_workspace(0, 64) == 0 and L.ternary_route_workspace(64, 512) == 0
+    assert L.ternary_route_workspace(0, 64) == 0 and L.ternary_route_workspace(32, 512) == 0 \
+        and L.ternary_route_workspace(64, 64) == 0
     assert L.ternary_route_workspace(65, 64) >= 5 * 64 * 2
     assert L.ternary_route_workspace(-1, 64) == SHAPE and L.ternary_route_workspace(5, 513) == SHAPE
     assert L.ternary_route_workspace(1 << 24, 512) > 0

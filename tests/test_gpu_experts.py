@@ -38,7 +38,7 @@ def check_route(tl, logits, k, score="softmax", bias=None, groups=1, top_groups=
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("T,E,k", [(0, 8, 2), (1, 1, 1), (1, 64, 8), (2, 3, 3), (15, 65, 6), (16, 128, 8), (17, 100, 1), (64, 512, 32), (65, 64, 8),
-                                   (63, 256, 10), (130, 129, 7), (333, 512, 32), (1000, 60, 4), (1024, 256, 8), (1, 512, 32), (1, 40, 32)])
+                                   (63, 256, 10), (32, 96, 5), (33, 96, 5), (33, 64, 5), (64, 64, 3), (4096, 40, 2), (4097, 40, 2), (130, 129, 7), (333, 512, 32), (1000, 60, 4), (1024, 256, 8), (1, 512, 32), (1, 40, 32)])
 def test_route(tl, T, E, k, score):
     rng = np.random.default_rng(T + E + k)
     logits = (2 * rng.standard_normal((T, E))).astype(np.float32)
