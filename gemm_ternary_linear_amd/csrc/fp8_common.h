@@ -10,7 +10,6 @@ namespace ternary {
 
 typedef unsigned int u32x4_v __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2_v __attribute__((ext_vector_type(2)));
-typedef int i32x8_v __attribute__((ext_vector_type(8)));
 
 constexpr float kE4m3Max = 448.f;
 

@@ -3,15 +3,20 @@
 //
 //     y[m, n] = sum_b xs[m, b] s(n, b) sum_{k in b} x[m, k] w[n, k]
 //
-// One v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 channels (the A operand)
-// by 16 rows of x (B) over one block of 128; its fp32 sums are then scaled and
-// added to the running sums, so no rounding but fp32's happens before the end.
+// Sums are fp32 throughout.  The matrix unit's 8-bit forms do not keep them: of eight products
+// that a lane holds side by side they align all to the largest and cut what falls 2^-14 below it, so
+// that beside a factor of 448 one of 2^-6 counts for nothing (measured; up to 2^-11.4 of the sum
+// of magnitudes, all of a sum whose large products cancel).  So both factors become fp16, which
+// holds every e4m3 value and +-2, and v_mfma_f32_16x16x32_f16 adds their products, which are exact, in 24 bits.
+// That unit has half the rate of the 8-bit one; what it costs is beside the kernels below.
+//
+// Four of those instructions multiply 16 channels (the A operand) by 16 rows of x (B) over one
+// block of 128; their sums are then scaled and added to the running sums.
 // A lane's four results are four channels of one row: the row's scale is one
-// register and the four go out in one store.  Ternary codes become fp4 (+-2) in five vector operations a 16 codes;
-// as those give a word's odd codes, then its even ones, x's bytes are put in the
-// same order (eight byte permutes per 16 rows x 128).  Lane group g (lanes 16 g
-// up) holds k = 32 g .. 32 g + 31 of a block of an fp4 operand, and k = 16 g .. and
-// 64 + 16 g .. (16 each) of an fp8 one.
+// register and the four go out in one store.  Ternary codes become fp4 (+-2) in five vector operations a 16 codes, and
+// fp16 by eight conversions; as the first give a word's odd codes, then its even ones, x's bytes are put in the
+// same order (eight byte permutes per 16 rows x 128).  A lane holds 32 values of k of each operand, the
+// same ones: of 8-bit weights k = 16 g .. and 64 + 16 g .. (16 each) in lane group g (lanes 16 g up).
 #include "fp8_common.h"
 #include "internal.h"
 
@@ -19,20 +24,17 @@ namespace ternary {
 
 namespace {
 
-// Whether outputs of a type take their sums from 16-bit operands.  The matrix unit
-// aligns the products of 32 8-bit (or fp4) factors to the largest before it adds them and
-// cuts what falls below: sums of a block were up to 2^-15.5 of the sum of magnitudes off
-// (random values over a few powers of two).  Rounding to bf16 or fp16 hides that; for fp32
-// outputs the factors become fp16 (exactly), whose products are added in full.
-constexpr bool wide_sums(int dtype) { return dtype == TERNARY_FP32; }
-
-// Eight e4m3 values (two registers), or eight fp4 values (one), as fp16.
+// A lane's 32 values of a block, for four instructions.
+struct Wide {
+    f16x8_t q[4];
+};
 template <class A>
 __device__ __forceinline__ f16x8_t join_halves(A a, A b, A c, A d)
 {
     return __builtin_bit_cast(f16x8_t, u32x4_v{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b),
                                               __builtin_bit_cast(uint32_t, c), __builtin_bit_cast(uint32_t, d)});
 }
+// Eight e4m3 values (two registers), or eight fp4 values (one), as fp16.
 __device__ __forceinline__ f16x8_t widen_fp8(int lo, int hi)
 {
     return join_halves(__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.f, false),
@@ -47,36 +49,26 @@ __device__ __forceinline__ f16x8_t widen_fp4(int v)
                        __builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)v, 1.f, 2),
                        __builtin_amdgcn_cvt_scalef32_pk_f16_fp4((uint32_t)v, 1.f, 3));
 }
-
-// One block of 128: 16 channels by 16 rows.  Without the instruction's own block
-// scales (both arguments 0) it issues faster: in a loop with the scaling of its results,
-// 4480 against 3883 TFLOP/s.  So an fp4 operand's +-2 stay, and half of each is left to
-// the channel's scale.  WIDE: by four 16-bit instructions of 32 each; what a lane holds of
-// w and x must be of the same k then.
-template <bool TERN, bool WIDE>
-__device__ __forceinline__ f32x4_t mfma(i32x8_v w, i32x8_v x)
+__device__ __forceinline__ Wide widen(u32x4_v a, u32x4_v b)
 {
-    f32x4_t d = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (WIDE) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            d = __builtin_amdgcn_mfma_f32_16x16x32_f16(TERN ? widen_fp4(w[q]) : widen_fp8(w[2 * q], w[2 * q + 1]),
-                                                       widen_fp8(x[2 * q], x[2 * q + 1]), d, 0, 0, 0);
-        return d;
-    } else {
-        return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, d, TERN ? 4 : 0, 0, 0, 0, 0, 0);
-    }
+    return Wide{{widen_fp8((int)a.x, (int)a.y), widen_fp8((int)a.z, (int)a.w), widen_fp8((int)b.x, (int)b.y),
+                 widen_fp8((int)b.z, (int)b.w)}};
+}
+
+// 32 of a block's k: 16 channels by 16 rows.
+__device__ __forceinline__ f32x4_t mfma(f16x8_t w, f16x8_t x, f32x4_t d)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(w, x, d, 0, 0, 0);
 }
 // Chunks of 16 of a block of x that lane group g holds: the first, and how many on
 // the second lies.  8-bit weights: as the same chunks of w; ternary ones: as the
-// instruction pairs them with the fp4 operand's lane groups, which hold the codes 0, 64, 32
-// and 96 (and 31 more), or (WIDE) those codes' own.
-template <bool TERN, bool WIDE>
+// lane groups of w hold the codes 0, 64, 32 and 96 (and 31 more).
+template <bool TERN>
 __device__ __forceinline__ int first_chunk(int g)
 {
-    return !TERN ? g : WIDE ? (g & 1) * 4 + (g & 2) : g + (g & 2);
+    return TERN ? (g & 1) * 4 + (g & 2) : g;
 }
-constexpr int second_chunk(bool tern, bool wide) { return !tern ? 4 : wide ? 1 : 2; }
+constexpr int second_chunk(bool tern) { return tern ? 1 : 4; }
 
 // Scale of a channel's fp4 products.
 __device__ __forceinline__ float channel_scale(uint16_t s) { return 0.5f * f16_bits_to_f32(s); }
@@ -156,24 +148,28 @@ __device__ __forceinline__ void codes_to_fp4(uint32_t w, int &odd, int &even)
     even = (int)((z << 2) & 0xccccccccu);
 }
 
-// 32 bytes of x in the order of the fp4 operand: per 16, odd then even.
-__device__ __forceinline__ i32x8_v odd_even(u32x4_v a, u32x4_v b)
+// 32 codes (two words) as fp16, per 16 odd then even.
+__device__ __forceinline__ Wide widen_codes(uint32_t w0, uint32_t w1)
 {
-    i32x8_v r;
-    r[0] = (int)__builtin_amdgcn_perm(a.y, a.x, 0x07050301u);
-    r[1] = (int)__builtin_amdgcn_perm(a.w, a.z, 0x07050301u);
-    r[2] = (int)__builtin_amdgcn_perm(a.y, a.x, 0x06040200u);
-    r[3] = (int)__builtin_amdgcn_perm(a.w, a.z, 0x06040200u);
-    r[4] = (int)__builtin_amdgcn_perm(b.y, b.x, 0x07050301u);
-    r[5] = (int)__builtin_amdgcn_perm(b.w, b.z, 0x07050301u);
-    r[6] = (int)__builtin_amdgcn_perm(b.y, b.x, 0x06040200u);
-    r[7] = (int)__builtin_amdgcn_perm(b.w, b.z, 0x06040200u);
-    return r;
+    int c[4];
+    codes_to_fp4(w0, c[0], c[1]);
+    codes_to_fp4(w1, c[2], c[3]);
+    return Wide{{widen_fp4(c[0]), widen_fp4(c[1]), widen_fp4(c[2]), widen_fp4(c[3])}};
 }
 
-__device__ __forceinline__ i32x8_v join(u32x4_v a, u32x4_v b)
+// 32 bytes of x in that order.
+__device__ __forceinline__ Wide widen_odd_even(u32x4_v a, u32x4_v b)
 {
-    return i32x8_v{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+    constexpr uint32_t odd = 0x07050301u, even = 0x06040200u;
+    return widen(u32x4_v{__builtin_amdgcn_perm(a.y, a.x, odd), __builtin_amdgcn_perm(a.w, a.z, odd),
+                         __builtin_amdgcn_perm(a.y, a.x, even), __builtin_amdgcn_perm(a.w, a.z, even)},
+                 u32x4_v{__builtin_amdgcn_perm(b.y, b.x, odd), __builtin_amdgcn_perm(b.w, b.z, odd),
+                         __builtin_amdgcn_perm(b.y, b.x, even), __builtin_amdgcn_perm(b.w, b.z, even)});
+}
+template <bool TERN>
+__device__ __forceinline__ Wide x_operand(u32x4_v a, u32x4_v b)
+{
+    return TERN ? widen_odd_even(a, b) : widen(a, b);
 }
 
 // Four channels ch .. ch + 3 of a row of y (those past N are left out).
@@ -256,10 +252,9 @@ __device__ __forceinline__ int swz(int r) { return r & 7; }
 // in neighbouring lanes) would cost a cache access per lane: at 45 rows of 18944 x 4096
 // the accesses of L1, not HBM, bounded a kernel that loaded x like w (39 us).
 //
-// Measured (kernel traces, bf16 outputs): 1 row of 4096 x 4096 5.7 us, of which an empty
-// launch is 1.9; 45 rows of 18944 x 4096 20.2 us (3.9 TB/s); 64 experts of 2048 x 4096, 8 a
-// token, 1 token 8.4 us, of which the launch and finding the experts 2.5; of 4096 x 1024
-// with scales per 128, 33 tokens, 23.1 us (3.2 TB/s).
+// Measured (calls in a graph, bf16 outputs; behind each the time with the 8-bit matrix instruction): 1 row of 4096 x
+// 4096 5.8 us (5.7); 45 rows of 18944 x 4096 21.4 (19.8; 3.7 TB/s); 64 experts of 2048 x 4096, 8 a
+// token, 1 token 8.5 (6.9), 16 tokens 46 (37); of 4096 x 1024 with scales per 128, 33 tokens, 31 (25; 2.4 TB/s).
 
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 // Blocks of a chunk: as many as leave room for two workgroups' x in a compute unit's LDS.
@@ -311,8 +306,8 @@ __device__ __forceinline__ void load_group_scales(const uint16_t *row, int b0, i
 }
 
 // TERN: ternary weights of experts (G: with group scales).
-template <bool TERN, bool G, bool WIDE, int MT, int FN>
-__global__ void __launch_bounds__(kThreads, FN * MT <= 8 ? 4 : 2) thin_kernel(const Fp8Product p, int ks)
+template <bool TERN, bool G, int MT, int FN>
+__global__ void __launch_bounds__(kThreads, FN < 3 ? 4 : 2) thin_kernel(const Fp8Product p, int ks)
 {
     constexpr int U = thin_chunk(MT);
     typedef float u_t __attribute__((ext_vector_type(U)));  // scales of a chunk
@@ -381,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, FN * MT <= 8 ? 4 : 2) thin_kernel(co
 #pragma unroll
     for (int j = 0; j < MT; ++j)
         sp[j] = p.x_scale + x_row(16 * j + col) * nb;
-    const int cg = first_chunk<TERN, WIDE>(g);
-    const int c0 = cg ^ (col & 7), c1 = (cg + second_chunk(TERN, WIDE)) ^ (col & 7);
+    const int cg = first_chunk<TERN>(g);
+    const int c0 = cg ^ (col & 7), c1 = (cg + second_chunk(TERN)) ^ (col & 7);
     lds_u4 *const lx = (lds_u4 *)sx + wave * (U * MT * 128);
     const int xa = (col >> 3) * 64 + (col & 7) * 8;
     constant_float *wsp[FN];  // w's scales of each fragment (16 channels are in one block)
@@ -443,49 +438,59 @@ __global__ void __launch_bounds__(kThreads, FN * MT <= 8 ? 4 : 2) thin_kernel(co
 #pragma unroll
         for (int j = 0; j < MT; ++j)
             xs[j] = ss[wave][j][col];
-        i32x8_v a[FN][2];
+        uint32_t odd[TERN ? FN : 1][2];  // codes of a slab's second block
         f32x4_t gs[FN];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int i = 0; i < FN; ++i) {
+            auto w_operand = [&](int i) -> Wide {
                 if constexpr (TERN) {
                     // A slab holds codes 64 q .. 64 q + 63 in lanes 16 q up; exchanging the
                     // halves of a wave (permlane32_swap) leaves a block's codes 0, 64, 32 and 96 (and
                     // 31 more) in its four lane groups.
-                    if (u % 2 == 0) {
-                        const u32x4_v r = w[i][u / 2];
-                        const u32x2_v lo = __builtin_amdgcn_permlane32_swap(r.x, r.z, false, false);
-                        const u32x2_v hi = __builtin_amdgcn_permlane32_swap(r.y, r.w, false, false);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            int c[4];
-                            codes_to_fp4(h ? lo.y : lo.x, c[0], c[1]);
-                            codes_to_fp4(h ? hi.y : hi.x, c[2], c[3]);
-                            a[i][h] = i32x8_v{c[0], c[1], c[2], c[3], 0, 0, 0, 0};
-                        }
-                    }
+                    if (u % 2)
+                        return widen_codes(odd[i][0], odd[i][1]);
+                    const u32x4_v r = w[i][u / 2];
+                    const u32x2_v lo = __builtin_amdgcn_permlane32_swap(r.x, r.z, false, false);
+                    const u32x2_v hi = __builtin_amdgcn_permlane32_swap(r.y, r.w, false, false);
+                    odd[i][0] = lo.y, odd[i][1] = hi.y;
+                    return widen_codes(lo.x, hi.x);
                 } else {
-                    a[i][u & 1] = join(w[i][2 * u], w[i][2 * u + 1]);
+                    return widen(w[i][2 * u], w[i][2 * u + 1]);
                 }
-            }
+            };
+            auto x_at = [&](int j) -> Wide {
+                return x_operand<TERN>(lx[(u * MT + j) * 128 + xa + c0], lx[(u * MT + j) * 128 + xa + c1]);
+            };
 #pragma unroll
             for (int i = 0; i < (G ? FN : 0); ++i) {
                 const u32x2_v q = *reinterpret_cast<const u32x2_v *>(&sg[wave][G ? u : 0][16 * i + 4 * g]);
                 gs[i] = f32x4_t{channel_scale((uint16_t)q.x), channel_scale((uint16_t)(q.x >> 16)),
                                 channel_scale((uint16_t)q.y), channel_scale((uint16_t)(q.y >> 16))};
             }
+            // Each fragment becomes fp16 once: the operand with fewer of them stays in registers.
+            constexpr bool KEEP_X = MT <= FN;
+            constexpr int KEPT = KEEP_X ? MT : FN, TURNS = KEEP_X ? FN : MT;
+            Wide kept[KEPT];
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-                const u32x4_v x0 = lx[(u * MT + j) * 128 + xa + c0], x1 = lx[(u * MT + j) * 128 + xa + c1];
-                const i32x8_v xv = TERN ? odd_even(x0, x1) : join(x0, x1);
+            for (int k = 0; k < KEPT; ++k)
+                kept[k] = KEEP_X ? x_at(k) : w_operand(k);
 #pragma unroll
-                for (int i = 0; i < FN; ++i) {
-                    const f32x4_t d = mfma<TERN, WIDE>(a[i][u & 1], xv);
+            for (int t = 0; t < TURNS; ++t) {
+                const Wide turn = KEEP_X ? w_operand(t) : x_at(t);
+                f32x4_t d[KEPT];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int k = 0; k < KEPT; ++k)
+                        d[k] = mfma(KEEP_X ? turn.q[q] : kept[k].q[q], KEEP_X ? kept[k].q[q] : turn.q[q],
+                                    q ? d[k] : f32x4_t{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int k = 0; k < KEPT; ++k) {
+                    const int i = KEEP_X ? t : k, j = KEEP_X ? k : t;
                     const float f = TERN ? xs[j][u] : xs[j][u] * ws[i][u];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        acc[i][j][k] += d[k] * (G ? f * gs[i][k] : f);
+                    for (int c = 0; c < 4; ++c)
+                        acc[i][j][c] += d[k][c] * (G ? f * gs[i][c] : f);
                 }
             }
         }
@@ -522,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, FN * MT <= 8 ? 4 : 2) thin_kernel(co
 
 // ks: ways to share K.  Each wave should have a chunk of its own, and the more
 // channels a workgroup holds the fewer there are, so no more ways than chunks.
-template <bool TERN, bool G, bool WIDE, int MT, int FN>
+template <bool TERN, bool G, int MT, int FN>
 hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 {
     constexpr int U = thin_chunk(MT);
@@ -531,7 +536,7 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
     const int64_t wgs = tiles * ((p.N + 16 * FN * (kWaves / ks) - 1) / (16 * FN * (kWaves / ks)));
     if (wgs > INT32_MAX)
         return hipErrorInvalidValue;
-    hipLaunchKernelGGL((thin_kernel<TERN, G, WIDE, MT, FN>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, p, ks);
+    hipLaunchKernelGGL((thin_kernel<TERN, G, MT, FN>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, p, ks);
     return hipGetLastError();
 }
 
@@ -554,47 +559,35 @@ inline int thin_fragments(int64_t frags, int most)
     return best;
 }
 
-template <bool TERN, bool G, bool WIDE, int MT>
+// Rows in tiles of 16 MT.
+template <bool TERN, bool G, int MT>
 hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 {
     const int64_t frags = (p.N + 15) / 16 * tiles;
     if constexpr (TERN) {
-        return frags < 1024 ? launch_thin<TERN, G, WIDE, MT, 1>(p, tiles, stream)
-                            : launch_thin<TERN, G, WIDE, MT, 2>(p, tiles, stream);
-    } else if constexpr (WIDE || MT == 1 || MT == 4) {
-        return frags <= device_cus() ? launch_thin<TERN, G, WIDE, MT, 1>(p, tiles, stream)
-                                     : launch_thin<TERN, G, WIDE, MT, 2>(p, tiles, stream);
+        return frags < 1024 ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
+                            : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
+    } else if constexpr (MT == 1 || MT == 4) {
+        return frags <= device_cus() ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
+                                     : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
     } else {
         switch (thin_fragments(frags, 5)) {
-        case 1: return launch_thin<TERN, G, WIDE, MT, 1>(p, tiles, stream);
-        case 2: return launch_thin<TERN, G, WIDE, MT, 2>(p, tiles, stream);
-        case 3: return launch_thin<TERN, G, WIDE, MT, 3>(p, tiles, stream);
-        default: return launch_thin<TERN, G, WIDE, MT, 5>(p, tiles, stream);
+        case 1: return launch_thin<TERN, G, MT, 1>(p, tiles, stream);
+        case 2: return launch_thin<TERN, G, MT, 2>(p, tiles, stream);
+        case 3: return launch_thin<TERN, G, MT, 3>(p, tiles, stream);
+        default: return launch_thin<TERN, G, MT, 5>(p, tiles, stream);
         }
     }
 }
 
-// Rows in tiles of 16 MT.
-template <bool TERN, int MT>
-hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
-{
-    auto run = [&](auto wide) {
-        constexpr bool W = decltype(wide)::value;
-        if constexpr (TERN)
-            return p.group ? launch_thin<true, true, W, MT>(p, tiles, stream)
-                           : launch_thin<true, false, W, MT>(p, tiles, stream);
-        else
-            return launch_thin<false, false, W, MT>(p, tiles, stream);
-    };
-    return wide_sums(p.dtype) ? run(std::true_type()) : run(std::false_type());
-}
-
 // ---------------------------------------------------------------- many rows
 
-// Measured (bf16 outputs; calls one after another): 2048 rows of 18944 x 4096 183 us (1.74
-// PFLOP/s; 168 to 188 between machines), the matrix unit busy for 58 % of the compute units'
-// cycles; 64 experts of 2048 x 4096, 8 a token, 2047 tokens, 205 us (1.34 PFLOP/s), busy for 37
-// %, at 3.3 times the vector instructions; 11 % of the tiles' places there have no row.
+// Measured (bf16 outputs; calls one after another): 2048 rows of 18944 x 4096 285 to 290 us (1.1
+// PFLOP/s; 183 with the 8-bit matrix instruction and its sums); 64 experts of 2048 x 4096, 8 a token, 2047
+// tokens, 305 to 313 us (0.89 PFLOP/s; 205); 11 % of the tiles' places there have no row.  Parts
+// left out in turn: without the conversions to fp16 265 and 235, without the scaling 268 and 291, without either
+// 250 and 230, at which the matrix unit's own rate is near (1.38 PFLOP/s in a bf16 library product).  Tiles of 256 channels x 128
+// rows took 296, of 128 x 256 301.
 
 // Tiles of TN channels x TM rows by WN x WM waves, NS stages deep.
 template <int TN_, int TM_, int WN_, int WM_, int NS_ = 2>
@@ -603,8 +596,9 @@ struct Tile {
     static_assert(NS == 2 || NS == 4);
     static constexpr int THREADS = WN * WM * 64;
     static constexpr int FN = TN / WN / 16, FM = TM / WM / 16;  // fragments of a wave
-    // waves a SIMD has registers for: one workgroup's, of 512 threads two
-    static constexpr int WAVES = THREADS / 256;
+    // Waves that a SIMD has registers for.  (With 512 registers a wave the compiler puts matrix results where
+    // vector instructions have to fetch them from: 310 instead of 290 us at 2048 x 18944 x 4096.)
+    static constexpr int WAVES = NS == 4 ? 1 : 2;  // (four stages leave LDS for one workgroup)
 };
 
 // Values b0 .. b0 + 3 of a row of n (past its end the last) that a whole workgroup reads.
@@ -615,10 +609,9 @@ __device__ __forceinline__ f32x4_t load_scales_uniform(const float *row, int b0,
 }
 
 // G: group-scaled ternary weights.
-template <bool TERN, bool G, int DT, class C>
+template <bool TERN, bool G, class C>
 __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Product p)
 {
-    constexpr bool WIDE = wide_sums(DT);
     constexpr int TN = C::TN, TM = C::TM, FN = C::FN, FM = C::FM, THREADS = C::THREADS, NS = C::NS;
     constexpr int XI = TM * 8 / THREADS;                      // x loads of a thread and stage
     constexpr int WCH = TERN ? TN * 2 : TN * 8;               // 16-byte chunks of w in a stage
@@ -787,21 +780,20 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
     // each (permlane32_swap) leaves a fragment with the codes 0, 64, 32 and 96 (and 31 more)
     // in its lane groups.
     static_assert(!TERN || FN % 2 == 0);
-    const int xa = (wm * FM * 16 + col) * 8, cg = first_chunk<TERN, WIDE>(g);
-    const int c0 = cg ^ swz(col), c1 = (cg + second_chunk(TERN, WIDE)) ^ swz(col);
+    const int xa = (wm * FM * 16 + col) * 8, cg = first_chunk<TERN>(g);
+    const int c0 = cg ^ swz(col), c1 = (cg + second_chunk(TERN)) ^ swz(col);
     const int wa = TERN ? wn * FN * 32 + lane : (wn * FN * 16 + col) * 8;
 
     // Operands on their way from LDS: w's two fragments ahead (ternary: two
     // fragments by one load), all of x's, and the scales.
     u32x4_v rw[2][2], rx[FM][2];
     fm_t fn, f, fp;          // the next step's, this step's, the last one's
-    // matrix results not yet scaled, and the fragments' channels' scales.  A
-    // result is scaled behind the second matrix instruction after its own: it is there by then.
-    constexpr int LAG = 2;
-    static_assert(FM >= LAG && FN * FM % 4 == 0);
-    f32x4_t d[4];
+    // The matrix results of this fragment and of the one before, which are scaled behind this one's
+    // matrix instructions: they are there by then.
+    f32x4_t d[2][FM];
     typedef float g_t __attribute__((ext_vector_type(G ? 4 * FN : 4)));
-    g_t gn, gs, gp;  // (the next step's, this step's, the last one's)
+    g_t gn, gs;  // its channels' scales: the next step's, this step's,
+    f32x4_t gp;  // the last one's last fragment's
     auto read_w = [&](auto S, int i) {
         constexpr int s = decltype(S)::value;
         if constexpr (TERN) {
@@ -824,7 +816,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
             gn = *reinterpret_cast<const g_t *>(sf + (b & 7) * SL + SF + (wn * 4 + g) * 4 * FN);
     };
     u32x2_v odd_codes = {0, 0};  // of the second fragment of two
-    auto w_operand = [&](int i) -> i32x8_v {
+    auto w_operand = [&](int i) -> Wide {
         if constexpr (TERN) {
             u32x2_v w = odd_codes;
             if (i % 2 == 0) {
@@ -834,43 +826,38 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
                 w = u32x2_v{lo.x, hi.x};
                 odd_codes = u32x2_v{lo.y, hi.y};
             }
-            int c[4];
-            codes_to_fp4(w.x, c[0], c[1]);
-            codes_to_fp4(w.y, c[2], c[3]);
-            return i32x8_v{c[0], c[1], c[2], c[3], 0, 0, 0, 0};
+            return widen_codes(w.x, w.y);
         } else {
-            return join(rw[i & 1][0], rw[i & 1][1]);
+            return widen(rw[i & 1][0], rw[i & 1][1]);
         }
     };
-    auto scale_add = [&](int n, const fm_t &by, bool last) {  // result n of this step, or of the last one
-        const int i = n / FM, j = n % FM;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            acc[i][j][k] += d[n & 3][k] * (G ? by[j] * (last ? gp : gs)[G ? 4 * i + k : 0] : by[j]);
+    // Value k of result j of fragment i of this step, or (i = -1) of the last one of the step before.
+    auto scale_add = [&](int i, int j, int k) {
+        const int c = i < 0 ? FN - 1 : i;
+        const float by = i < 0 ? fp[j] : f[j];
+        acc[c][j][k] += d[c & 1][j][k] * (G ? by * (i < 0 ? gp[k] : gs[G ? 4 * c + k : 0]) : by);
     };
 
-    // Step b, from stage s.  Each matrix instruction is followed by the scaling of a
-    // result of the fragment before, so that neither waits for the other.  The
+    // Step b, from stage s.  A fragment is four matrix instructions a row fragment, by turns; each is
+    // followed by the scaling of a value of the fragment before, so that neither waits for the other.
+    // x's fragments become fp16 once a step, in front of their first instruction.  The
     // waves meet two fragments before the end, once the stage is read and the next one is there:
-    // from then on this stage takes step b + NS, and the next step's first
-    // operands are read behind the last fragments' matrix instructions.  The
-    // stage's loads are spread from there over the first fragments of the next
-    // step: issued together they hold up the waves, whose turns in the load unit
-    // come one after another.
-    constexpr int ROWS = FN >= 8 ? 4 : 1, LATE = NP / 2 < ROWS ? NP / 2 : ROWS, EARLY = NP - LATE;
+    // from then on this stage takes step b + NS, its loads spread over the instructions (issued
+    // together they hold up the waves, whose turns in the load unit come one after another), and
+    // the next step's first operands are read behind the last fragments' matrix instructions.
     auto step = [&](auto S, int b) {
         constexpr int s = decltype(S)::value;
-        constexpr std::integral_constant<int, (s + 1) % NS> T;       // the next step's stage
-        constexpr std::integral_constant<int, (s + NS - 1) % NS> L;  // the last step's
+        constexpr std::integral_constant<int, (s + 1) % NS> T;  // the next step's stage
         static_assert(FN % 2 == 0 && FN >= 4);
-        i32x8_v x[FM];
+        Wide x[FM];
         fp = f;
         f = fn;
-        gp = gs;
+        if constexpr (G)
+            gp = f32x4_t{gs[G ? 4 * FN - 4 : 0], gs[G ? 4 * FN - 3 : 0], gs[G ? 4 * FN - 2 : 0], gs[G ? 4 * FN - 1 : 0]};
         gs = gn;
 #pragma unroll
         for (int i = 0; i < FN; ++i) {
-            const i32x8_v a = w_operand(i);
+            const Wide a = w_operand(i);
             if (i == FN - 2) {
                 meet<(NS - 2) * NP>();
                 read_f(b + 1);
@@ -889,26 +876,25 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
             }
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int j = 0; j < FM; ++j) {
-                const int n = i * FM + j;
-                if (i == 0)
-                    x[j] = TERN ? odd_even(rx[j][0], rx[j][1]) : join(rx[j][0], rx[j][1]);
-                asm volatile("" : "+v"(x[j]));  // (nothing: keeps the instruction from moving up)
-                d[n & 3] = mfma<TERN, WIDE>(a, x[j]);
-                if (i == FN - 1)
-                    read_x(T, j);
-                const int m = n >= LAG ? n - LAG : n - LAG + FN * FM;
-                scale_add(m, n >= LAG ? f : fp, n < LAG);
-                if (j == 1 && i < LATE)
-                    issue(L, min(b + NS - 1, nb - 1), EARLY + i);
-                if (i >= FN - 2)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                    for (int q = 0; q < NP; ++q)
-                        if (q < EARLY && q % (2 * FM) == (i - (FN - 2)) * FM + j)
-                            issue(S, min(b + NS, nb - 1), q);
-                asm volatile("" : "+v"(acc[m / FM][m % FM]));  // (the same, down)
-                __builtin_amdgcn_sched_barrier(0);
-            }
+                for (int j = 0; j < FM; ++j) {
+                    if (i == 0 && q == 0)
+                        x[j] = x_operand<TERN>(rx[j][0], rx[j][1]);
+                    asm volatile("" : "+v"(x[j].q[q]));  // (nothing: keeps the instruction from moving up)
+                    d[i & 1][j] = mfma(a.q[q], x[j].q[q], q ? d[i & 1][j] : zero);
+                    if (i == FN - 1 && q == 3)
+                        read_x(T, j);
+                    scale_add(i - 1, j, q);
+                    constexpr int SLOTS = 8 * FM;  // instructions of the last two fragments
+                    const int slot = (i - (FN - 2)) * 4 * FM + q * FM + j;
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+                        if (i >= FN - 2 && slot == n * SLOTS / NP)
+                            issue(S, min(b + NS, nb - 1), n);
+                    asm volatile("" : "+v"(acc[i ? i - 1 : FN - 1][j]));  // (the same, down)
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             if (i + 2 < FN)
                 read_w(S, i + 2);
             else
@@ -919,22 +905,21 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
     // Every step loads a stage for NS steps on; the last ones load the last step
     // again, into a stage that is not read (a branch there, or a second exit of the loop, had
     // the compiler copy the step).
-    auto fill = [&](auto S, int count) {
+    auto fill = [&](auto S) {
         constexpr int s = decltype(S)::value;
 #pragma unroll
         for (int q = 0; q < NP; ++q)
-            if (q < count)
-                issue(S, min(s, nb - 1), q);
+            issue(S, min(s, nb - 1), q);
     };
-    fill(std::integral_constant<int, 0>(), NP);
+    fill(std::integral_constant<int, 0>());
     if constexpr (NS == 4) {
-        fill(std::integral_constant<int, 1>(), NP);
-        fill(std::integral_constant<int, 2>(), NP);
+        fill(std::integral_constant<int, 1>());
+        fill(std::integral_constant<int, 2>());
     }
     next = load_factors(0);
     store_factors(next, 0);
     meet<(NS - 2) * NP>();
-    fill(std::integral_constant<int, NS - 1>(), EARLY);
+    fill(std::integral_constant<int, NS - 1>());
     read_w(std::integral_constant<int, 0>(), 0);
     read_w(std::integral_constant<int, 0>(), 1);
     read_f(0);
@@ -942,9 +927,10 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
     for (int j = 0; j < FM; ++j) {
         read_x(std::integral_constant<int, 0>(), j);
         f[j] = 0.f;
+        d[1][j] = zero;  // (as a last fragment of a step before)
     }
-    d[2] = d[3] = zero;
     gs = 0.f;
+    gp = zero;
     if constexpr (!G)
         gn = 0.f;
     int b = 0;
@@ -965,8 +951,10 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
             step(std::integral_constant<int, 2>(), b + 2);
     }
 #pragma unroll
-    for (int n = FN * FM - LAG; n < FN * FM; ++n)
-        scale_add(n, f, false);
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            scale_add(FN - 1, j, k);
     meet<0>();  // no load into LDS outlives the workgroup
 
 #pragma unroll
@@ -981,7 +969,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
         for (int j = 0; j < FM; ++j) {
             const int row = r0 + (wm * FM + j) * 16 + col;
             if (row < r1)
-                put4<DT>(p, row, ch, TERN && !G ? acc[i][j] * cs : acc[i][j]);
+                put4(p, row, ch, TERN && !G ? acc[i][j] * cs : acc[i][j]);
         }
     }
 }
@@ -993,13 +981,10 @@ hipError_t launch_tiles(const Fp8Product &p, int64_t tiles, hipStream_t stream)
     const int64_t wgs = TERN ? (tiles + 7) / 8 * 8 * ntn : (tiles * ntn + 7) / 8 * 8;
     if (wgs > INT32_MAX)
         return hipErrorInvalidValue;
-    with_dtype(p.dtype, [&](auto dt) {
-        constexpr int DT = wide_sums(decltype(dt)::value) && C::FN * C::FM > 16 ? TERNARY_BF16 : decltype(dt)::value;
-        if (TERN && p.group)
-            hipLaunchKernelGGL((tile_kernel<TERN, TERN, DT, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
-        else
-            hipLaunchKernelGGL((tile_kernel<TERN, false, DT, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
-    });
+    if (TERN && p.group)
+        hipLaunchKernelGGL((tile_kernel<TERN, TERN, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
+    else
+        hipLaunchKernelGGL((tile_kernel<TERN, false, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -1031,28 +1016,25 @@ double rounds_of(int64_t n, int64_t most)
 hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
 {
     if (p.M <= 16)
-        return launch_thin<false, 1>(p, 1, stream);
+        return launch_thin<false, false, 1>(p, 1, stream);
     if (p.M <= 32)
-        return launch_thin<false, 2>(p, 1, stream);
+        return launch_thin<false, false, 2>(p, 1, stream);
     if (p.M <= 48)
-        return launch_thin<false, 3>(p, 1, stream);
-    const int64_t cus = device_cus(), m64 = (p.M + 63) / 64, m128 = (p.M + 127) / 128, m256 = (p.M + 255) / 256;
-    const int64_t n128 = ((int64_t)p.N + 127) / 128, n256 = ((int64_t)p.N + 255) / 256, frags = m64 * ((p.N + 15) / 16);
+        return launch_thin<false, false, 3>(p, 1, stream);
+    const int64_t cus = device_cus(), m64 = (p.M + 63) / 64, m128 = (p.M + 127) / 128;
+    const int64_t n128 = ((int64_t)p.N + 127) / 128, frags = m64 * ((p.N + 15) / 16);
     const double t_thin = 1.0 + p.nb * (frags <= cus ? 0.178 : 0.237 * rounds_of((frags + 1) / 2, cus));
     const double t_64 = p.nb * (m64 * n128 <= cus ? 0.48 : 0.85 * rounds_of(m64 * n128, 2 * cus));
     const double t_128 = p.nb * (m128 * n128 <= cus ? 0.72 : 1.2 * rounds_of(m128 * n128, 2 * cus));
-    const double t_256 = p.nb * 1.75 * rounds_of(m256 * n256, cus);
-    if (t_thin <= t_64 && t_thin <= t_128 && (t_thin <= t_256 || wide_sums(p.dtype)))
-        return launch_thin<false, 4>(p, m64, stream);
-    if (t_64 <= t_128 && (t_64 <= t_256 || wide_sums(p.dtype))) {
+    if (t_thin <= t_64 && t_thin <= t_128)
+        return launch_thin<false, false, 4>(p, m64, stream);
+    if (t_64 <= t_128) {
         // Four stages take so much LDS that a compute unit holds one workgroup: for one round.
         // 64 rows of 18944 x 4096: 18.1 us, with two stages 23.7; 512 rows of 4096 x 4096 17.2 and 21.6.
         return m64 * n128 <= cus ? launch_tiles<false, Tile<128, 64, 2, 2, 4>>(p, m64, stream)
                                  : launch_tiles<false, Tile<128, 64, 2, 2>>(p, m64, stream);
     }
-    if (t_128 <= t_256 || wide_sums(p.dtype))  // (16-bit operands leave no registers for larger tiles)
-        return launch_tiles<false, Tile<128, 128, 2, 2>>(p, m128, stream);
-    return launch_tiles<false, Tile<256, 256, 2, 4>>(p, m256, stream);
+    return launch_tiles<false, Tile<128, 128, 2, 2>>(p, m128, stream);
 }
 
 // Few places an expert: streamed, K shared by eight waves; else tiles of 64
@@ -1065,7 +1047,8 @@ hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
 hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream)
 {
     if (p.M <= (p.nb >= 16 ? 8 : 16) * (int64_t)p.E)
-        return launch_thin<true, 1>(p, expert_tiles(p, 16), stream);
+        return p.group ? launch_thin<true, true, 1>(p, expert_tiles(p, 16), stream)
+                       : launch_thin<true, false, 1>(p, expert_tiles(p, 16), stream);
     return launch_tiles<true, Tile<128, 64, 2, 2>>(p, expert_tiles(p, 64), stream);
 }
 

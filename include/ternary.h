@@ -408,11 +408,9 @@ int ternary_fp8_quantize(const void *x, int dtype, int64_t M, int64_t K, int64_t
  * x and w 16-byte, the scales 4-byte aligned.  For each block of 128 along K
  * the products are exact and summed; x_scale * w_scale (an fp32
  * product) multiplies the block's sum and the blocks are added in fp32, in an
- * order that depends on M, N, K and dtype alone; y is rounded once, to nearest even.
- * A block's sum is fp32 for fp32 outputs.  For 16-bit outputs the matrix unit
- * adds the products of 32 factors after cutting them at a common place: sums came out within 2^-15 of
- * the sum of the products' magnitudes (a 16-bit output's own rounding is 2^-9 or 2^-12
- * of its value).
+ * order that depends on M, N and K alone; y is rounded once, to nearest even.
+ * Sums are fp32 for every dtype: each of a block's 128 additions keeps 24 bits of the
+ * block's sum of magnitudes, or more (it may cut what lies below instead of rounding).
  * A NaN code or scale gives NaN in every output that reads it.
  */
 int ternary_fp8_linear(const uint8_t *x, const float *x_scale, const uint8_t *w,
@@ -495,9 +493,9 @@ typedef enum {
  *   y           [R, N] output, dtype `dtype` (TERNARY_BF16, TERNARY_FP16 or
  *               TERNARY_FP32), 16-byte aligned; must not overlap any input.
  * x and tiled 16-byte, x_scale, offsets and order 4-byte, scale 2-byte aligned.  For each block
- * of 128 along K the products are exact and summed (as by ternary_fp8_linear); sums of blocks are
- * multiplied by their scales and added in fp32, in an order that depends on
- * the sizes and dtype alone, and y is rounded once.  `offsets` must ascend from 0 to at most R and
+ * of 128 along K the products are exact and summed in fp32 (as by ternary_fp8_linear, for every
+ * dtype); sums of blocks are multiplied by their scales and added in fp32, in an order that depends on
+ * the sizes alone, and y is rounded once.  `offsets` must ascend from 0 to at most R and
  * `order` name rows of x: entries that do not are not followed (no memory outside the
  * arguments is touched), the outputs that they concern are unspecified.
  */
