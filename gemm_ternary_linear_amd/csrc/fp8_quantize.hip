@@ -30,14 +30,15 @@ __device__ __forceinline__ u32x2_v codes8(const float v[8], float s)
     float r[8];
     // The rounded quotient: by one reciprocal (corrected once) and, for each value, a
     // product whose exact remainder corrects it.  Three operations a value where a division takes
-    // ten; remainders stay exact while s is neither tiny nor huge.
+    // ten; remainders stay exact while s is neither tiny nor huge.  (The correction of a -0 is +0: the sign
+    // is put back.)
     const bool mid = s > 0x1p-100f && s < 0x1p100f;
     if (__builtin_amdgcn_ballot_w64(!mid) == 0) {
         const float a = __builtin_amdgcn_rcpf(s), inv = fmaf(fmaf(-s, a, 1.f), a, a);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float q = v[i] * inv;
-            r[i] = fmaf(fmaf(-s, q, v[i]), inv, q);  // (at most 448)
+            r[i] = copysignf(fmaf(fmaf(-s, q, v[i]), inv, q), v[i]);  // (at most 448)
         }
     } else {
 #pragma unroll
@@ -67,7 +68,7 @@ __device__ __forceinline__ float swiglu(float g, float u)
     const bool far = fabsf(t) > 100.f;
     const float d = 1.f + (far ? e : fmaf(e, rest * 0x1.62e43p-1f, e));
     const float r = __builtin_amdgcn_rcpf(d), q = g * r;
-    return (far ? q : fmaf(fmaf(-d, q, g), r, q)) * u;
+    return copysignf(far ? q : fmaf(fmaf(-d, q, g), r, q), g) * u;  // (the sign of -0)
 }
 
 // Values k .. k+7 of a row (columns from K on are zeros).  VEC: 16-byte loads
