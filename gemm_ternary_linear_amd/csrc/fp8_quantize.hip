@@ -13,8 +13,9 @@
 // maximum a butterfly over those lanes, so a wave does four blocks at a time
 // with no LDS; a weight tile is a workgroup, eight rows a lane.
 //
-// Measured (kernel trace, bf16): 16384 x 1024 SwiGLU 18.5 us for 84 MB (4.5 TB/s, part of it
-// from cache between repeats; a copy of 2 GiB 4.9); 1 x 4096 2.1 us, an empty launch 1.9.
+// Measured (calls in a graph, bf16): 16384 x 1024 SwiGLU 16.9 us for 84 MB (5.0 TB/s, part of it
+// from cache between repeats; a copy of 2 GiB 4.9); 18944 x 4096 in tiles 41.6 us for 233 MB (likewise); 1 x 4096 2.2 us, an
+// empty launch 1.9.
 #include "fp8_common.h"
 #include "internal.h"
 
@@ -56,19 +57,45 @@ __device__ __forceinline__ u32x2_v codes8(const float v[8], float s)
     return u32x2_v{(uint32_t)a, (uint32_t)b};
 }
 
-// silu(g) * u, silu within about two roundings: exp(-g) as a power of two whose
-// argument's rounding (up to |g| 2^-24 of the result) is put back, and a quotient by a
-// corrected reciprocal.  From 2^100 on, and below 2^-100, exp(-g) is taken as it comes
-// (infinity: silu is 0; 0: silu is g): there t or the remainder may be infinite.
+// silu(g) * u, silu within about three roundings: (g > 0 ? g : g E) / (1 + E) with E = exp(-|g|),
+// which nothing overflows.  E is a power of two whose argument's rounding (up to |g| 2^-24 of the
+// result) is put back, the quotient one by a corrected reciprocal.  FAR: for gates past 20
+// (the rest get the same bits), where the divisor is 1; past 80 E is taken 2^64 times larger until u is in, as exp2
+// gives nothing below 2^-126 and a subnormal silu would be rounded to few bits.
+template <bool FAR>
 __device__ __forceinline__ float swiglu(float g, float u)
 {
+#pragma clang fp contract(off)  // (t + 64 has to be t's rounded value, to which `rest` belongs, and 64)
     const float hi = 0x1.715476p+0f, lo = 0x1.4ae0cp-26f;  // log2(e), and what fp32 leaves of it
-    const float t = -g * hi, rest = fmaf(-g, hi, -t) - g * lo;
-    const float e = __builtin_amdgcn_exp2f(t);
-    const bool far = fabsf(t) > 100.f;
-    const float d = 1.f + (far ? e : fmaf(e, rest * 0x1.62e43p-1f, e));
-    const float r = __builtin_amdgcn_rcpf(d), q = g * r;
-    return copysignf(far ? q : fmaf(fmaf(-d, q, g), r, q), g) * u;  // (the sign of -0)
+    const float a = FAR ? fminf(fabsf(g), 300.f) : fabsf(g);  // (E is 0 by then; a NaN stays in g)
+    const float t = -a * hi, rest = fmaf(-a, lo, fmaf(-a, hi, -t));
+    const bool small = FAR && a > 80.f;
+    const float e = __builtin_amdgcn_exp2f(small ? t + 64.f : t);
+    const float E = fmaf(e, rest * 0x1.62e43p-1f, e), n = g > 0.f ? g : g * E;
+    const float d = 1.f + E, r = __builtin_amdgcn_rcpf(d), q = n * r;
+    const float near = copysignf(fmaf(fmaf(-d, q, n), r, q), g);  // (the correction of a -0 is +0)
+    if constexpr (!FAR)
+        return near * u;
+    const float v = (a > 20.f ? n : near) * u;
+    return small && !(g > 0.f) ? v * 0x1p-64f : v;
+}
+
+// The same of eight, v the gates.
+__device__ __forceinline__ void swiglu8(float v[8], const float u[8])
+{
+    bool near = true;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        near = near && fabsf(v[i]) <= 20.f;
+    if (__builtin_amdgcn_ballot_w64(!near) == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = swiglu<false>(v[i], u[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = swiglu<true>(v[i], u[i]);
+    }
 }
 
 // Values k .. k+7 of a row (columns from K on are zeros).  VEC: 16-byte loads
@@ -76,6 +103,7 @@ __device__ __forceinline__ float swiglu(float g, float u)
 template <int DT, bool SWIGLU, bool VEC>
 __device__ __forceinline__ void values8(const void *x, int64_t row, int K, int k, float v[8])
 {
+    float u[8];
     if constexpr (VEC) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -83,24 +111,21 @@ __device__ __forceinline__ void values8(const void *x, int64_t row, int K, int k
         if (k >= K)
             return;
         load8<DT>(x, row + k, v);
-        if constexpr (SWIGLU) {
-            float u[8];
+        if constexpr (SWIGLU)
             load8<DT>(x, row + K + k, u);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                v[i] = swiglu(v[i], u[i]);
-        }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[i] = 0.f;
+            v[i] = u[i] = 0.f;
             if (k + i < K) {
                 v[i] = load_elem<DT>(x, row + k + i);
                 if constexpr (SWIGLU)
-                    v[i] = swiglu(v[i], load_elem<DT>(x, row + K + k + i));
+                    u[i] = load_elem<DT>(x, row + K + k + i);
             }
         }
     }
+    if constexpr (SWIGLU)
+        swiglu8(v, u);
 }
 
 // The largest magnitude (NaN left out; 0 where nothing is left).
