@@ -291,7 +291,7 @@ __device__ __forceinline__ void load_scales(const float *row, int b0, int n, flo
 typedef uint16_t u16x4_u __attribute__((ext_vector_type(4), aligned(2)));
 
 // Group scales (fp16) of blocks b0 .. b0 + U - 1 of a channel of n groups of `gb`
-// blocks; past its end the last.
+// blocks; past its end 0.
 template <int U>
 __device__ __forceinline__ void load_group_scales(const uint16_t *row, int b0, int gb, int n, uint16_t v[U])
 {
@@ -302,6 +302,9 @@ __device__ __forceinline__ void load_group_scales(const uint16_t *row, int b0, i
 #pragma unroll
         for (int i = 0; i < U; ++i)
             v[i] = row[min((b0 + i) / gb, n - 1)];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            v[i] = (b0 + i) / gb < n ? v[i] : (uint16_t)0;
     }
 }
 
@@ -392,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, FN < 3 ? 4 : 2) thin_kernel(const Fp
         for (int j = 0; j < MT; ++j)
             acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-    // Blocks past the last load that again, and count with scale 0.
+    // Blocks past the last load that again, and count with scales of 0 (all of them: 0 times an infinite one is NaN).
     for (int b0 = kpart * U; b0 < nb; b0 += ks * U) {
         float ws[FN][U];
 #pragma unroll
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, FN < 3 ? 4 : 2) thin_kernel(const Fp
             for (int i = 0; i < FN; ++i)
 #pragma unroll
                 for (int u = 0; u < U; ++u)
-                    ws[i][u] = wsp[i][min(b0 + u, nb - 1)];
+                    ws[i][u] = b0 + u < nb ? wsp[i][min(b0 + u, nb - 1)] : 0.f;
         if constexpr (G)
             if (lane < 16 * FN) {  // a channel a lane
                 uint16_t v[U];
