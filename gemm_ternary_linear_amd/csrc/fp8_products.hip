@@ -324,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, FN < 3 ? 4 : 2) thin_kernel(const Fp
     const int nb = p.nb, kpart = wave % ks, parts = kWaves / ks;
     // workgroups run over the channels first: those of one tile of rows are neighbours
     const int ntn = (p.N + 16 * FN * parts - 1) / (16 * FN * parts);
-    const int tm = blockIdx.x / ntn, n0 = ((blockIdx.x - tm * ntn) * parts + wave / ks) * 16 * FN;
+    const int slot = blockIdx.x / ntn, tm = TERN ? p.first + slot : slot;
+    const int n0 = ((blockIdx.x - slot * ntn) * parts + wave / ks) * 16 * FN;
     int e = 0, r0 = tm * 16 * MT, r1 = min(p.M, r0 + 16 * MT);
     if constexpr (TERN)
         if (!find_tile<16 * MT>(p.offsets, p.E, p.M, tm, e, r0, r1))
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, FN < 3 ? 4 : 2) thin_kernel(const Fp
         for (int w = 1; w < ks; ++w)
             s += red[w0 + w][fr][lane];
         const int row = r0 + 16 * j + col;
-        const int ch = ((blockIdx.x - tm * ntn) * parts + q / (FN * MT)) * 16 * FN + 16 * i + 4 * g;
+        const int ch = ((blockIdx.x - slot * ntn) * parts + q / (FN * MT)) * 16 * FN + 16 * i + 4 * g;
         if (row >= r1)
             continue;
         if constexpr (TERN && !G)
@@ -528,6 +529,21 @@ __global__ void __launch_bounds__(kThreads, FN < 3 ? 4 : 2) thin_kernel(const Fp
     }
 }
 
+// Most threads of a launch, and `tiles` tiles of rows in launches of at most `most` each.
+constexpr int64_t kMostThreads = (int64_t)1 << 31;
+template <class F>
+hipError_t launch_pieces(const Fp8Product &p, int64_t tiles, int64_t most, F launch)
+{
+    hipError_t e = hipSuccess;
+    for (int64_t t = 0; t < tiles && e == hipSuccess; t += most) {
+        Fp8Product part = p;
+        part.first = (int)t;
+        launch(part, tiles - t < most ? tiles - t : most);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
 // ks: ways to share K.  Each wave should have a chunk of its own, and the more
 // channels a workgroup holds the fewer there are, so no more ways than chunks.
 template <bool TERN, bool G, int MT, int FN>
@@ -536,11 +552,11 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
     constexpr int U = thin_chunk(MT);
     const int chunks = (p.nb + U - 1) / U;
     const int ks = chunks >= 8 ? 8 : chunks >= 4 ? 4 : chunks >= 2 ? 2 : 1;
-    const int64_t wgs = tiles * ((p.N + 16 * FN * (kWaves / ks) - 1) / (16 * FN * (kWaves / ks)));
-    if (wgs > INT32_MAX)
-        return hipErrorInvalidValue;
-    hipLaunchKernelGGL((thin_kernel<TERN, G, MT, FN>), dim3((unsigned)wgs), dim3(kThreads), 0, stream, p, ks);
-    return hipGetLastError();
+    const int64_t ntn = (p.N + 16 * FN * (kWaves / ks) - 1) / (16 * FN * (kWaves / ks));
+    // 8-bit weights: a tile of at most 48 rows, or up to 2^18 tiles of few channels: one launch
+    return launch_pieces(p, tiles, TERN ? kMostThreads / kThreads / ntn : tiles, [&](const Fp8Product &part, int64_t n) {
+        hipLaunchKernelGGL((thin_kernel<TERN, G, MT, FN>), dim3((unsigned)(n * ntn)), dim3(kThreads), 0, stream, part, ks);
+    });
 }
 
 // Fragments of 16 channels a wave holds: F with the fewest rounds of F over the
@@ -648,7 +664,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
     const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3;
     int tm, tn;
     if constexpr (TERN) {
-        tm = slot / ntn * 8 + xcd;
+        tm = p.first + slot / ntn * 8 + xcd;
         tn = slot % ntn;
     } else {
         const int ntm = (p.M + TM - 1) / TM;
@@ -981,14 +997,22 @@ template <bool TERN, class C>
 hipError_t launch_tiles(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 {
     const int ntn = (p.N + C::TN - 1) / C::TN;
-    const int64_t wgs = TERN ? (tiles + 7) / 8 * 8 * ntn : (tiles * ntn + 7) / 8 * 8;
-    if (wgs > INT32_MAX)
-        return hipErrorInvalidValue;
-    if (TERN && p.group)
-        hipLaunchKernelGGL((tile_kernel<TERN, TERN, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
-    else
-        hipLaunchKernelGGL((tile_kernel<TERN, false, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
-    return hipGetLastError();
+    if constexpr (TERN) {
+        // (whole eights of tiles a launch: tile t runs on XCD t % 8)
+        return launch_pieces(p, tiles, kMostThreads / C::THREADS / ntn & ~(int64_t)7, [&](const Fp8Product &part, int64_t n) {
+            const dim3 grid((unsigned)((n + 7) / 8 * 8 * ntn));
+            if (p.group)
+                hipLaunchKernelGGL((tile_kernel<true, true, C>), grid, dim3(C::THREADS), 0, stream, part);
+            else
+                hipLaunchKernelGGL((tile_kernel<true, false, C>), grid, dim3(C::THREADS), 0, stream, part);
+        });
+    } else {
+        const int64_t wgs = (tiles * ntn + 7) / 8 * 8;
+        if (wgs * C::THREADS > UINT32_MAX)
+            return hipErrorInvalidValue;  // (an output of more than 2^37 elements)
+        hipLaunchKernelGGL((tile_kernel<false, false, C>), dim3((unsigned)wgs), dim3(C::THREADS), 0, stream, p);
+        return hipGetLastError();
+    }
 }
 
 // Tiles of `rows` places that E experts of R places in all can need.

@@ -206,6 +206,7 @@ struct Fp8Product {
     // experts only
     const int32_t *offsets, *order;  // order: NULL where x holds the places themselves
     int E, group, ngroups, top_k, x_rows;
+    int first;  // the launch's first tile of rows
 };
 hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream);
 hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream);
