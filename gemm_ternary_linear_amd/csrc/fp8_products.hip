@@ -199,14 +199,12 @@ __device__ __forceinline__ void put4(const Fp8Product &p, int row, int ch, f32x4
         put4<TERNARY_FP32>(p, row, ch, s);
 }
 
-// Waits for all but the last N of this wave's loads from memory (those into LDS
-// among them) and for its LDS reads, then for the workgroup's other waves.
-template <int N>
+// Waits for this wave's loads from memory (those into LDS among them) and for its LDS
+// reads, then for the workgroup's other waves.
 __device__ __forceinline__ void meet()
 {
-    static_assert(N >= 0 && N < 64);
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 7 << 4);  // vmcnt(N) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(7 << 4);  // vmcnt(0) lgkmcnt(0)
     asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
 }
@@ -559,20 +557,22 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
     });
 }
 
-// Fragments of 16 channels a wave holds: F with the fewest rounds of F over the
-// compute units, the larger of two (it reads x less often).  18944 x 4096 at 45
-// rows: F = 5 19.2 us, 3 22.6, 2 24.7, 1 26.5; 8192 x 4096: F = 2 10.0, 1 12.6, 5
-// 17.4; 4096 x 4096: F = 1 8.0, 2 9.7.  Where a chunk is long (one fragment of
-// rows) or x takes much of LDS (four) F = 2 is the most that pays (8 rows
-// of 18944 x 4096: F = 1 to 3 about 20 us, 5 31; 64 rows: F = 2 28.3, 5 33.1).
-inline int thin_fragments(int64_t frags, int most)
+// Fragments of 16 channels a wave holds, 17 to 48 rows: F with the fewest rounds of F over the
+// compute units, the larger of two (it reads x less often).  us, 45 rows (F = 1 to 5): 18944 x 4096
+// 27.2, 26.3, 25.5, 29.6, 21.0; 16384 x 4096 23.0, 19.9, 24.8, 18.5, 20.0; 12288 x 4096 18.6, 18.9, 14.9,
+// 17.0, 18.9; 8192 x 2048 8.3, 7.6, 8.7, 10.2, 11.0; 4096 x 4096 8.5, 10.6, 13.3, 15.2, 17.3.  Up to 16 rows a chunk
+// is long, two workgroups share a compute unit and F = 1 is the best or near it (8 rows, F = 1 to 3: 18944 x 4096
+// 19.5, 20.7, 20.0; 12288 x 4096 12.8, 12.4, 11.4; 8192 x 2048 5.8, 7.9, 9.9; 1024 x 8192 7.4, 12.6, 16.8).  64 rows: F = 1 where
+// that is one round (4096 x 4096: 10.2, with 2 12.2), else 2 (18944 x 4096: 1 34.0, 2 29.3, 3 29.3; 128 rows of 4096 x
+// 4096 16.7, 12.7, 15.9; 12288 x 4096 22.9, 21.2, 17.2, but 192 rows of 4096 x 1024 9.3, 8.5, 12.9).
+inline int thin_fragments(int64_t frags)
 {
     const int64_t cus = device_cus();
     int best = 1;
     int64_t least = INT64_MAX;
-    for (int f = 1; f <= most; ++f) {
+    for (int f = 1; f <= 5; ++f) {
         const int64_t rounds = (frags + f * cus - 1) / (f * cus) * f;
-        if (rounds <= least && f != 4)
+        if (rounds <= least)
             least = rounds, best = f;
     }
     return best;
@@ -586,14 +586,17 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
     if constexpr (TERN) {
         return frags < 1024 ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
                             : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
-    } else if constexpr (MT == 1 || MT == 4) {
+    } else if constexpr (MT == 1) {
+        return launch_thin<TERN, G, MT, 1>(p, tiles, stream);
+    } else if constexpr (MT == 4) {
         return frags <= device_cus() ? launch_thin<TERN, G, MT, 1>(p, tiles, stream)
                                      : launch_thin<TERN, G, MT, 2>(p, tiles, stream);
     } else {
-        switch (thin_fragments(frags, 5)) {
+        switch (thin_fragments(frags)) {
         case 1: return launch_thin<TERN, G, MT, 1>(p, tiles, stream);
         case 2: return launch_thin<TERN, G, MT, 2>(p, tiles, stream);
         case 3: return launch_thin<TERN, G, MT, 3>(p, tiles, stream);
+        case 4: return launch_thin<TERN, G, MT, 4>(p, tiles, stream);
         default: return launch_thin<TERN, G, MT, 5>(p, tiles, stream);
         }
     }
@@ -608,16 +611,15 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 // 250 and 230, at which the matrix unit's own rate is near (1.38 PFLOP/s in a bf16 library product).  Tiles of 256 channels x 128
 // rows took 296, of 128 x 256 301.
 
-// Tiles of TN channels x TM rows by WN x WM waves, NS stages deep.
-template <int TN_, int TM_, int WN_, int WM_, int NS_ = 2>
+// Tiles of TN channels x TM rows by WN x WM waves.
+template <int TN_, int TM_, int WN_, int WM_>
 struct Tile {
-    static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_, NS = NS_;
-    static_assert(NS == 2 || NS == 4);
+    static constexpr int TN = TN_, TM = TM_, WN = WN_, WM = WM_;
     static constexpr int THREADS = WN * WM * 64;
     static constexpr int FN = TN / WN / 16, FM = TM / WM / 16;  // fragments of a wave
     // Waves that a SIMD has registers for.  (With 512 registers a wave the compiler puts matrix results where
     // vector instructions have to fetch them from: 310 instead of 290 us at 2048 x 18944 x 4096.)
-    static constexpr int WAVES = NS == 4 ? 1 : 2;  // (four stages leave LDS for one workgroup)
+    static constexpr int WAVES = 2;
 };
 
 // Values b0 .. b0 + 3 of a row of n (past its end the last) that a whole workgroup reads.
@@ -631,7 +633,7 @@ __device__ __forceinline__ f32x4_t load_scales_uniform(const float *row, int b0,
 template <bool TERN, bool G, class C>
 __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Product p)
 {
-    constexpr int TN = C::TN, TM = C::TM, FN = C::FN, FM = C::FM, THREADS = C::THREADS, NS = C::NS;
+    constexpr int TN = C::TN, TM = C::TM, FN = C::FN, FM = C::FM, THREADS = C::THREADS;
     constexpr int XI = TM * 8 / THREADS;                      // x loads of a thread and stage
     constexpr int WCH = TERN ? TN * 2 : TN * 8;               // 16-byte chunks of w in a stage
     constexpr int WI = (WCH + THREADS - 1) / THREADS;
@@ -639,10 +641,10 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
     static_assert(TM * 8 % THREADS == 0 && (WCH % THREADS == 0 || WI == 1) && TM <= THREADS && TN <= THREADS);
     // One object per stage (x, then w): a load into one stage is then known not to
     // touch the others.
-    constexpr int STAGE = TM * 8 + WCH, S2 = NS > 2 ? STAGE : 1;
-    __shared__ __attribute__((aligned(16))) u32x4_v st0[STAGE], st1[STAGE], st2[S2], st3[S2];
-    lds_u4 *const lx[4] = {(lds_u4 *)st0, (lds_u4 *)st1, (lds_u4 *)st2, (lds_u4 *)st3};
-    lds_u4 *const lw[4] = {lx[0] + TM * 8, lx[1] + TM * 8, lx[2] + (NS > 2 ? TM * 8 : 0), lx[3] + (NS > 2 ? TM * 8 : 0)};
+    constexpr int STAGE = TM * 8 + WCH;
+    __shared__ __attribute__((aligned(16))) u32x4_v st0[STAGE], st1[STAGE];
+    lds_u4 *const lx[2] = {(lds_u4 *)st0, (lds_u4 *)st1};
+    lds_u4 *const lw[2] = {lx[0] + TM * 8, lx[1] + TM * 8};
     // Scales of eight steps: x's (times w's for 8-bit weights), a lane's FM rows
     // together, then a group's channels', a lane's FN fragments together.  They are read
     // and written right behind the waves' meeting: the compiler waits for every load into
@@ -861,12 +863,12 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
     // followed by the scaling of a value of the fragment before, so that neither waits for the other.
     // x's fragments become fp16 once a step, in front of their first instruction.  The
     // waves meet two fragments before the end, once the stage is read and the next one is there:
-    // from then on this stage takes step b + NS, its loads spread over the instructions (issued
+    // from then on this stage takes step b + 2, its loads spread over the instructions (issued
     // together they hold up the waves, whose turns in the load unit come one after another), and
     // the next step's first operands are read behind the last fragments' matrix instructions.
     auto step = [&](auto S, int b) {
         constexpr int s = decltype(S)::value;
-        constexpr std::integral_constant<int, (s + 1) % NS> T;  // the next step's stage
+        constexpr std::integral_constant<int, 1 - s> T;  // the next step's stage
         static_assert(FN % 2 == 0 && FN >= 4);
         Wide x[FM];
         fp = f;
@@ -878,15 +880,10 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
         for (int i = 0; i < FN; ++i) {
             const Wide a = w_operand(i);
             if (i == FN - 2) {
-                meet<(NS - 2) * NP>();
+                meet();
                 read_f(b + 1);
                 // scales ahead: loaded at the first step of four, put into LDS at the third
-                if constexpr (NS == 4) {
-                    if (s == 0)
-                        next = load_factors(b + 4);
-                    if (s == 2)
-                        store_factors(next, b + 2);
-                } else if constexpr (s == 0) {
+                if constexpr (s == 0) {
                     if (b & 2)
                         store_factors(next, b + 2);
                     else
@@ -910,7 +907,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
 #pragma unroll
                     for (int n = 0; n < NP; ++n)
                         if (i >= FN - 2 && slot == n * SLOTS / NP)
-                            issue(S, min(b + NS, nb - 1), n);
+                            issue(S, min(b + 2, nb - 1), n);
                     asm volatile("" : "+v"(acc[i ? i - 1 : FN - 1][j]));  // (the same, down)
                     __builtin_amdgcn_sched_barrier(0);
                 }
@@ -921,7 +918,7 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
         }
     };
 
-    // Every step loads a stage for NS steps on; the last ones load the last step
+    // Every step loads a stage for two steps on; the last ones load the last step
     // again, into a stage that is not read (a branch there, or a second exit of the loop, had
     // the compiler copy the step).
     auto fill = [&](auto S) {
@@ -931,14 +928,10 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
             issue(S, min(s, nb - 1), q);
     };
     fill(std::integral_constant<int, 0>());
-    if constexpr (NS == 4) {
-        fill(std::integral_constant<int, 1>());
-        fill(std::integral_constant<int, 2>());
-    }
     next = load_factors(0);
     store_factors(next, 0);
-    meet<(NS - 2) * NP>();
-    fill(std::integral_constant<int, NS - 1>());
+    meet();
+    fill(std::integral_constant<int, 1>());
     read_w(std::integral_constant<int, 0>(), 0);
     read_w(std::integral_constant<int, 0>(), 1);
     read_f(0);
@@ -953,28 +946,18 @@ __global__ void __launch_bounds__(C::THREADS, C::WAVES) tile_kernel(const Fp8Pro
     if constexpr (!G)
         gn = 0.f;
     int b = 0;
-    for (; b + NS <= nb; b += NS) {
+    for (; b + 2 <= nb; b += 2) {
         step(std::integral_constant<int, 0>(), b);
         step(std::integral_constant<int, 1>(), b + 1);
-        if constexpr (NS == 4) {
-            step(std::integral_constant<int, 2>(), b + 2);
-            step(std::integral_constant<int, 3>(), b + 3);
-        }
     }
     if (b < nb)
         step(std::integral_constant<int, 0>(), b);
-    if constexpr (NS == 4) {
-        if (b + 1 < nb)
-            step(std::integral_constant<int, 1>(), b + 1);
-        if (b + 2 < nb)
-            step(std::integral_constant<int, 2>(), b + 2);
-    }
 #pragma unroll
     for (int j = 0; j < FM; ++j)
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             scale_add(FN - 1, j, k);
-    meet<0>();  // no load into LDS outlives the workgroup
+    meet();  // no load into LDS outlives the workgroup
 
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
@@ -1021,10 +1004,6 @@ int64_t expert_tiles(const Fp8Product &p, int rows)
     return p.M / rows + (p.M < p.E ? p.M : p.E);
 }
 
-}  // namespace
-
-namespace {
-
 // Expected time of n tiles in rounds of `most`, as a multiple of a round's: between
 // whole rounds and an even spread.
 double rounds_of(int64_t n, int64_t most)
@@ -1032,14 +1011,21 @@ double rounds_of(int64_t n, int64_t most)
     return ((double)((n + most - 1) / most) + (n > most ? (double)n / most : 1.0)) / 2;
 }
 
+// Row tiles of `rows` that R places of E experts are expected to need: an expert's last is half full.
+int64_t likely_tiles(const Fp8Product &p, int rows)
+{
+    const int64_t most = p.M < p.E ? p.M : p.E, n = p.M / rows + most / 2;
+    return n > most ? n : most;
+}
+
 }  // namespace
 
-// Which kernel: the least of what each is expected to take, from its time a
-// block of K (us, measured over M = 64 .. 2048 at 18944 x 4096, 4096 x 4096 and 1024 x 8192;
-// the estimates are within 25 % there).  Measured sides, us: 64 rows of 4096 x 4096 streamed 9.3,
-// tiles of 64 rows 15; of 18944 x 4096 28 and 23.5; 192 rows of 1024 x 8192 12.7 and 25; 384 rows
-// of 18944 x 4096 tiles of 64 52, 128 39, 256 56; 1024 rows 124, 97, 110; 2048 rows
-// 218, 180, 172.
+// Which kernel: the least of what each is expected to take (us), fitted to times over M = 64 .. 4096 at
+// 18944, 16384, 12288, 4096 and 256 x 4096, 1024 x 8192, 8192 x 2048 and 4096 x 1024; what it
+// chose there was at most 7 % over the best.  Streamed, tiles of 64 rows and of 128, us: 64 rows of 4096 x 4096 10.2, 24.1 and 35.0; of
+// 18944 x 4096 29.3, 25.5 and 35.9; 192 rows of 1024 x 8192 13.9, 43.8 and 64.3; 384 rows of 18944 x 4096 (tiles) 70.9
+// and 59.4; 2048 rows 322 and 289; 4096 rows of 256 x 4096 26.8, 25.0 and 35.6.  Four stages of 64 rows instead of two were slower
+// at every one of them (64 rows of 18944 x 4096 26.3, 192 rows 50.6 against 37.4).
 hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
 {
     if (p.M <= 16)
@@ -1049,34 +1035,37 @@ hipError_t launch_fp8_linear(const Fp8Product &p, hipStream_t stream)
     if (p.M <= 48)
         return launch_thin<false, false, 3>(p, 1, stream);
     const int64_t cus = device_cus(), m64 = (p.M + 63) / 64, m128 = (p.M + 127) / 128;
-    const int64_t n128 = ((int64_t)p.N + 127) / 128, frags = m64 * ((p.N + 15) / 16);
-    const double t_thin = 1.0 + p.nb * (frags <= cus ? 0.178 : 0.237 * rounds_of((frags + 1) / 2, cus));
-    const double t_64 = p.nb * (m64 * n128 <= cus ? 0.48 : 0.85 * rounds_of(m64 * n128, 2 * cus));
-    const double t_128 = p.nb * (m128 * n128 <= cus ? 0.72 : 1.2 * rounds_of(m128 * n128, 2 * cus));
+    const int64_t n128 = ((int64_t)p.N + 127) / 128, frags = m64 * (((int64_t)p.N + 15) / 16);
+    const double t_thin = 1.0 + (frags <= cus ? 0.24 * p.nb : (1.2 + 0.28 * p.nb) * rounds_of((frags + 1) / 2, cus));
+    const double t_64 = 3.0 + p.nb * (m64 * n128 <= cus ? 0.66 : 1.06 * rounds_of(m64 * n128, 2 * cus));
+    const double t_128 = 5.0 + p.nb * (m128 * n128 <= cus ? 0.93 : 1.75 * rounds_of(m128 * n128, 2 * cus));
     if (t_thin <= t_64 && t_thin <= t_128)
         return launch_thin<false, false, 4>(p, m64, stream);
-    if (t_64 <= t_128) {
-        // Four stages take so much LDS that a compute unit holds one workgroup: for one round.
-        // 64 rows of 18944 x 4096: 18.1 us, with two stages 23.7; 512 rows of 4096 x 4096 17.2 and 21.6.
-        return m64 * n128 <= cus ? launch_tiles<false, Tile<128, 64, 2, 2, 4>>(p, m64, stream)
-                                 : launch_tiles<false, Tile<128, 64, 2, 2>>(p, m64, stream);
-    }
+    if (t_64 <= t_128)
+        return launch_tiles<false, Tile<128, 64, 2, 2>>(p, m64, stream);
     return launch_tiles<false, Tile<128, 128, 2, 2>>(p, m128, stream);
 }
 
-// Few places an expert: streamed, K shared by eight waves; else tiles of 64
-// places.  64 experts, 8 a token, us, streamed and tiles: 2048 x 4096 at 1 token 9.0 and
-// 20, 16 tokens 37 and 47, 64 47 and 48, 128 62 and 48; 4096 x 1024 (scales per 128) at 16
-// 23 and 28, 128 36 and 38, 256 56 and 41.  Four stages took 193 instead of 171 us at
-// 2047 tokens of 4096 x 1024 (fewer workgroups a compute unit), tiles of 128 places 155,
-// but 207 instead of 200 of 2048 x 4096 and 59 instead of 41 at 256 tokens: an expert's last
-// tile is half empty on average.
+// Likewise: streamed, K shared by eight waves, or tiles of 64 or 128 places; the latter from 112 places an
+// expert on (with fewer an expert's only tile is seldom full).  Fitted at 64 experts of 2048 x 4096 and 4096 x 1024 (scales per
+// 128), 16 of 1024 x 2048 and 128 of 512 x 2048 (per 128), 8 a token, 1 to 2047 tokens; at most 6 % over the best there.  us,
+// streamed, 64 and 128: 2048 x 4096 at 16 tokens 44, 71 and 113, 100 68, 74 and 115, 128 78, 75 and 116, 1024 (tiles) 201 and 178, 2047
+// 335 and 295; 4096 x 1024 at 128 46, 48 and 75, 192 58, 52 and 77, 2047 219 and 192; 16 of 1024 x 2048 at 64 12, 17 and 24.
 hipError_t launch_linear_experts(const Fp8Product &p, hipStream_t stream)
 {
-    if (p.M <= (p.nb >= 16 ? 8 : 16) * (int64_t)p.E)
-        return p.group ? launch_thin<true, true, 1>(p, expert_tiles(p, 16), stream)
-                       : launch_thin<true, false, 1>(p, expert_tiles(p, 16), stream);
-    return launch_tiles<true, Tile<128, 64, 2, 2>>(p, expert_tiles(p, 64), stream);
+    const int64_t cus = device_cus(), n128 = ((int64_t)p.N + 127) / 128;
+    const int64_t t64 = likely_tiles(p, 64) * n128, t128 = likely_tiles(p, 128) * n128;
+    const bool group = p.group != 0;
+    const double t_thin = 3.0 + p.nb * (group ? 0.23 : 0.20) * likely_tiles(p, 16) * p.N / 32 / (2 * cus);
+    const double t_64 = 3.0 + p.nb * (t64 <= cus ? 0.84 : (group ? 1.45 : 1.15) * rounds_of(t64, 2 * cus));
+    const double t_128 = 5.0 + p.nb * (t128 <= cus ? 1.1 : (group ? 2.3 : 1.85) * rounds_of(t128, 2 * cus));
+    const bool full = p.M >= 112 * (int64_t)p.E;
+    if (t_thin <= t_64 && (t_thin <= t_128 || !full))
+        return group ? launch_thin<true, true, 1>(p, expert_tiles(p, 16), stream)
+                     : launch_thin<true, false, 1>(p, expert_tiles(p, 16), stream);
+    if (t_64 <= t_128 || !full)
+        return launch_tiles<true, Tile<128, 64, 2, 2>>(p, expert_tiles(p, 64), stream);
+    return launch_tiles<true, Tile<128, 128, 2, 2>>(p, expert_tiles(p, 128), stream);
 }
 
 }  // namespace ternary

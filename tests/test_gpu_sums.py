@@ -37,7 +37,10 @@ def outliers(rng, x, big):
 
 # every kernel of the products: few rows, then tiles of rows of each size
 @pytest.mark.parametrize("M,N,K", [(1, 48, 512), (8, 80, 1024), (16, 4112, 128), (20, 100, 384), (33, 129, 256), (60, 200, 1664), (64, 18944, 128),
-                                   (70, 16500, 256), (500, 1100, 384), (384, 6000, 256), (1030, 2050, 256), (2048, 2304, 128)])
+                                   (70, 16500, 256), (500, 1100, 384), (384, 6000, 256), (1030, 2050, 256), (2048, 2304, 128),
+                                   # 17 to 48 rows: one to five fragments of channels a wave (on 256 compute units)
+                                   (17, 8192, 256), (25, 12288, 384), (32, 16384, 128), (31, 18944, 256), (40, 8192, 128), (48, 12200, 256), (45, 16384, 384),
+                                   (41, 18950, 256), (130, 8200, 384), (3000, 4100, 384)])
 def test_linear_outliers(tl, M, N, K):
     """Products of 2^16, cancelling, beside others of 225/64: every partial sum is a multiple of 2^-6 below 2^17, so
     sums of 24 bits are exact in any order, and every output bit is known."""
@@ -54,7 +57,9 @@ def test_linear_outliers(tl, M, N, K):
 
 @pytest.mark.parametrize("rows", ["tokens", "sorted"])
 @pytest.mark.parametrize("T,E,k,N,K,g", [(1, 8, 2, 64, 512, -1), (2, 4, 2, 100, 384, 128), (9, 3, 1, 4112, 256, 256), (40, 16, 4, 33, 2048, -1),
-                                         (200, 4, 2, 300, 640, -1), (300, 5, 2, 140, 512, 128), (700, 3, 2, 272, 768, 256)])
+                                         (200, 4, 2, 300, 640, -1), (300, 5, 2, 140, 512, 128), (700, 3, 2, 272, 768, 256),
+                                         # tiles of 128 places
+                                         (3000, 4, 2, 2100, 512, -1), (3001, 4, 2, 2100, 640, 128), (2000, 4, 3, 2050, 768, 256)])
 def test_experts_outliers(tl, T, E, k, N, K, g, rows):
     """Factors of 448, cancelling, beside others of 7 x 2^-9: partial sums are multiples of 2^-9 below 2^10."""
     say(f"experts outliers {T} {E} {k} {N} {K} g={g} {rows}")
