@@ -40,7 +40,7 @@ def outliers(rng, x, big):
                                    (70, 16500, 256), (500, 1100, 384), (384, 6000, 256), (1030, 2050, 256), (2048, 2304, 128),
                                    # 17 to 48 rows: one to five fragments of channels a wave (on 256 compute units)
                                    (17, 8192, 256), (25, 12288, 384), (32, 16384, 128), (31, 18944, 256), (40, 8192, 128), (48, 12200, 256), (45, 16384, 384),
-                                   (41, 18950, 256), (130, 8200, 384), (3000, 4100, 384)])
+                                   (41, 18950, 256), (130, 8200, 384), (3000, 4100, 384), (381, 18943, 1152)])
 def test_linear_outliers(tl, M, N, K):
     """Products of 2^16, cancelling, beside others of 225/64: every partial sum is a multiple of 2^-6 below 2^17, so
     sums of 24 bits are exact in any order, and every output bit is known."""
