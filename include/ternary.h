@@ -409,8 +409,8 @@ int ternary_fp8_quantize(const void *x, int dtype, int64_t M, int64_t K, int64_t
  * the products are exact and summed; x_scale * w_scale (an fp32
  * product) multiplies the block's sum and the blocks are added in fp32, in an
  * order that depends on M, N and K alone; y is rounded once, to nearest even.
- * Sums are fp32 for every dtype: each of a block's 128 additions keeps 24 bits of the
- * block's sum of magnitudes, or more (it may cut what lies below instead of rounding).
+ * Sums are fp32 for every dtype: each of a block's 128 additions is off by at most 2^-23 of
+ * the block's sum of magnitudes (the matrix unit may cut what lies below instead of rounding).
  * A NaN code or scale gives NaN in every output that reads it.
  */
 int ternary_fp8_linear(const uint8_t *x, const float *x_scale, const uint8_t *w,
