@@ -251,8 +251,8 @@ __device__ __forceinline__ int swz(int r) { return r & 7; }
 // the accesses of L1, not HBM, bounded a kernel that loaded x like w (39 us).
 //
 // Measured (calls in a graph, bf16 outputs; behind each the time with the 8-bit matrix instruction): 1 row of 4096 x
-// 4096 5.8 us (5.7); 45 rows of 18944 x 4096 21.4 (19.8; 3.7 TB/s); 64 experts of 2048 x 4096, 8 a
-// token, 1 token 8.5 (6.9), 16 tokens 46 (37); of 4096 x 1024 with scales per 128, 33 tokens, 31 (25; 2.4 TB/s).
+// 4096 5.6 us (5.7); 45 rows of 18944 x 4096 20.7 (19.8; 3.8 TB/s); 64 experts of 2048 x 4096, 8 a
+// token, 1 token 8.0 (6.9), 16 tokens 44 (37); of 4096 x 1024 with scales per 128, 33 tokens, 31 (25; 2.4 TB/s).
 
 constexpr int kWaves = 8, kThreads = kWaves * 64;
 // Blocks of a chunk: as many as leave room for two workgroups' x in a compute unit's LDS.
@@ -605,11 +605,11 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 // ---------------------------------------------------------------- many rows
 
 // Measured (bf16 outputs; calls one after another): 2048 rows of 18944 x 4096 285 to 290 us (1.1
-// PFLOP/s; 183 with the 8-bit matrix instruction and its sums); 64 experts of 2048 x 4096, 8 a token, 2047
-// tokens, 305 to 313 us (0.89 PFLOP/s; 205); 11 % of the tiles' places there have no row.  Parts
-// left out in turn: without the conversions to fp16 265 and 235, without the scaling 268 and 291, without either
-// 250 and 230, at which the matrix unit's own rate is near (1.38 PFLOP/s in a bf16 library product).  Tiles of 256 channels x 128
-// rows took 296, of 128 x 256 301.
+// PFLOP/s; 183 with the 8-bit matrix instruction and its sums), the matrix unit busy for 58 % of the compute units' cycles; 64
+// experts of 2048 x 4096, 8 a token, 2047 tokens, 288 to 300 us (0.93 PFLOP/s; 205), busy for 51 %.  Parts
+// left out in turn (experts in tiles of 64 places, 308): without the conversions to fp16 265 and 235, without the scaling 268 and 291,
+// without either 250 and 230, at which the matrix unit's own rate is near (1.38 PFLOP/s in a bf16 library product).  Tiles of 256
+// channels x 128 rows took 296, of 128 x 256 301.
 
 // Tiles of TN channels x TM rows by WN x WM waves.
 template <int TN_, int TM_, int WN_, int WM_>
