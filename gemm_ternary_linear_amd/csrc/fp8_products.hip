@@ -564,7 +564,9 @@ hipError_t launch_thin(const Fp8Product &p, int64_t tiles, hipStream_t stream)
 // is long, two workgroups share a compute unit and F = 1 is the best or near it (8 rows, F = 1 to 3: 18944 x 4096
 // 19.5, 20.7, 20.0; 12288 x 4096 12.8, 12.4, 11.4; 8192 x 2048 5.8, 7.9, 9.9; 1024 x 8192 7.4, 12.6, 16.8).  64 rows: F = 1 where
 // that is one round (4096 x 4096: 10.2, with 2 12.2), else 2 (18944 x 4096: 1 34.0, 2 29.3, 3 29.3; 128 rows of 4096 x
-// 4096 16.7, 12.7, 15.9; 12288 x 4096 22.9, 21.2, 17.2, but 192 rows of 4096 x 1024 9.3, 8.5, 12.9).
+// 4096 16.7, 12.7, 15.9; 12288 x 4096 22.9, 21.2, 17.2, but 192 rows of 4096 x 1024 9.3, 8.5, 12.9).  Experts: F = 1 below 1024
+// fragments (1 token, 8 of 16 of 1024 x 2048: 5.2, with 2 5.9; of 128 of 512 x 2048 5.5 and 6.4), else 2 (8 of 64 of 2048 x 4096
+// 12.1 and 8.7; 16 tokens 66.8 and 44.4).
 inline int thin_fragments(int64_t frags)
 {
     const int64_t cus = device_cus();
