@@ -30,7 +30,8 @@ __all__ = [
     "probe_mfma", "probe_mfma_flops", "probe_lib", "PROBE_LIB_PATH", "quantize",
     "linear_batch_noalloc", "tile", "untile",
     "tiled_bytes", "LAYOUTS", "fp8_quantize", "fp8_linear", "route", "Routing", "linear_experts",
-    "combine",
+    "combine", "sort_slots", "dispatch", "dispatch_backward", "combine_backward", "linear_adapters",
+    "linear_adapters_backward",
 ]
 
 LIB_PATH = Path(__file__).resolve().parent / "libternary.so"
@@ -50,6 +51,10 @@ EXPORTS = (
     "ternary_linear_batch_noalloc", "ternary_tile", "ternary_untile", "ternary_tiled_bytes",
     "ternary_linear_tiled", "ternary_fp8_quantize", "ternary_fp8_linear", "ternary_route",
     "ternary_route_workspace", "ternary_linear_experts", "ternary_combine",
+    "ternary_sort_slots", "ternary_sort_slots_workspace", "ternary_dispatch",
+    "ternary_dispatch_backward", "ternary_combine_backward", "ternary_linear_adapters",
+    "ternary_linear_adapters_workspace", "ternary_linear_adapters_backward",
+    "ternary_linear_adapters_backward_workspace",
 )
 # Every symbol include/ternary_probe.h declares (measurement probes).
 PROBE_EXPORTS = ("ternary_probe_read", "ternary_probe_read_nt", "ternary_probe_copy",
@@ -106,6 +111,19 @@ def lib() -> ctypes.CDLL:
     L.ternary_linear_experts.argtypes = [p, p, i64, p, p, i64, i64, i64, i64, p, p, i64, i32, i32, p,
                                          i32, p]
     L.ternary_combine.argtypes = [p, i32, i64, i64, p, p, i64, i32, p, p, p]
+    L.ternary_sort_slots.argtypes = [p, i64, i32, i64, p, p, p, p, p, p]
+    L.ternary_dispatch.argtypes = [p, i32, i64, i64, p, p, i32, i64, p, p]
+    L.ternary_dispatch_backward.argtypes = [p, i32, i64, i64, p, p, i64, i32, p, p, p, p, p]
+    L.ternary_combine_backward.argtypes = [p, p, i32, i64, i64, p, p, i64, i32, p, p, p]
+    L.ternary_linear_adapters.argtypes = [p, i32, i64, i64, i64, i64, p, p, i64, p, p, p, p, p, p, p, p, p]
+    L.ternary_linear_adapters_backward.argtypes = [p, p, p, i32, i64, i64, i64, i64, p, p, i64, p, p, p, p,
+                                                   p, p, p, p, p, p]
+    L.ternary_sort_slots_workspace.argtypes = [i64, i32, i64]
+    for nm in ("ternary_linear_adapters_workspace", "ternary_linear_adapters_backward_workspace"):
+        getattr(L, nm).argtypes = [i64, i64, i64, i64, i64]
+    for nm in ("ternary_sort_slots_workspace", "ternary_linear_adapters_workspace",
+               "ternary_linear_adapters_backward_workspace"):
+        getattr(L, nm).restype = i64
     L.ternary_select_path.argtypes = [i64, i64, i64, i64]
     L.ternary_status_string.argtypes = [i32]
     L.ternary_status_string.restype = ctypes.c_char_p
@@ -114,7 +132,9 @@ def lib() -> ctypes.CDLL:
                "ternary_abi_version", "ternary_shutdown", "ternary_quantize",
                "ternary_linear_batch_noalloc", "ternary_linear_tiled", "ternary_tile",
                "ternary_untile", "ternary_fp8_quantize", "ternary_fp8_linear", "ternary_route",
-               "ternary_linear_experts", "ternary_combine"):
+               "ternary_linear_experts", "ternary_combine", "ternary_sort_slots", "ternary_dispatch",
+               "ternary_dispatch_backward", "ternary_combine_backward", "ternary_linear_adapters",
+               "ternary_linear_adapters_backward"):
         getattr(L, nm).restype = i32
     _lib = L
     return L
@@ -622,6 +642,173 @@ def combine(y: torch.Tensor, routing: Routing, add: torch.Tensor | None = None,
     _call("ternary_combine", dev, y.data_ptr(), dt, R, N, routing.slots.data_ptr(),
           routing.weights.data_ptr(), T, k, add.data_ptr() if add is not None else None, out.data_ptr())
     return out
+
+
+# ---------------------------------------------------------------- sorted slots, the exchange's gradients, adapters
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _workspace(name: str, like: torch.Tensor, *sizes):
+    """A new workspace of the size that library function `name` gives; None where it needs none."""
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    need = fn(*sizes)
+    if need < 0:
+        raise TernaryError(need, name.removesuffix("_workspace"))
+    return like.new_empty(need, dtype=torch.uint8) if need else None
+
+
+def sort_slots(ids: torch.Tensor, experts: int, weights: torch.Tensor | None = None) -> Routing:
+    """A Routing of given indices: ids int32 [T, top_k], each slot's expert (another router's choice), or [T] or [T, 1],
+    each token's adapter; an id outside [0, experts) holds none (ternary_sort_slots).  ``weights`` (float32
+    [T, top_k]; 1 if not given) and ``ids`` are passed on as they are."""
+    if ids.dtype != torch.int32 or ids.dim() not in (1, 2):
+        raise ValueError("ids must be an int32 tensor [T, top_k] or [T]")
+    if ids.dim() == 1:
+        ids = ids.unsqueeze(1)
+    T, k = ids.shape
+    if weights is not None and (weights.dtype != torch.float32 or weights.shape != (T, k)):
+        raise ValueError(f"weights must be a float32 tensor [{T}, {k}]")
+    dev = _same_device(ids, ids, weights)
+    ones = weights is None
+    # (held until the launches are enqueued, as route() does)
+    ws = _workspace("ternary_sort_slots_workspace", ids, T, k, experts)
+    if ones:
+        weights = ids.new_empty((T, k), dtype=torch.float32)
+    offsets, order, slots = ids.new_empty(experts + 1), ids.new_empty(T * k), torch.empty_like(ids)
+    _call("ternary_sort_slots", dev, ids.data_ptr(), T, k, experts, weights.data_ptr() if ones else None,
+          offsets.data_ptr(), order.data_ptr(), slots.data_ptr(), _ptr(ws))
+    return Routing(ids, weights, offsets, order, slots)
+
+
+def _rows_of(t: torch.Tensor, rows: int, name: str):
+    """The dtype code and row length of `t`, a matrix of `rows` rows."""
+    dt = _OUT.get(t.dtype)
+    if dt is None or t.dim() != 2 or t.shape[0] != rows:
+        raise ValueError(f"{name} must be a bfloat16, float16 or float32 tensor of {rows} rows")
+    return dt, t.shape[1]
+
+
+def _match(t: torch.Tensor | None, shape: tuple, dtype: torch.dtype, name: str):
+    if t is not None and (t.dtype != dtype or t.shape != shape):
+        raise ValueError(f"{name} must be a {str(dtype)[6:]} tensor of shape {list(shape)}")
+
+
+def dispatch(x: torch.Tensor, routing: Routing, weighted: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """out [T * top_k, N]: at each place of ``routing.order`` the token's row of x [T, N], with ``weighted`` times the
+    slot's weight, in x's dtype (bf16, fp16 or fp32; ternary_dispatch): the rows that experts take with
+    ``rows="sorted"``.  Rows of places that hold no slot are not written.  combine() is the way back."""
+    T, k = _check_routing(routing)
+    dt, N = _rows_of(x, T, "x")
+    dev = _same_device(x, x, routing.slots, routing.weights)
+    out = _output(out, (T * k, N), x.dtype, dev, x)
+    if out.dtype != x.dtype:
+        raise ValueError("out must have x's dtype")
+    _call("ternary_dispatch", dev, x.data_ptr(), dt, T, N, routing.slots.data_ptr(),
+          routing.weights.data_ptr() if weighted else None, k, T * k, out.data_ptr())
+    return out
+
+
+def dispatch_backward(grad: torch.Tensor, routing: Routing, x: torch.Tensor | None = None,
+                      add: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """The gradient of dispatch(): grad [T * top_k, N] is that of its result, which gives dx [T, N], plus ``add`` (another
+    gradient of x; may be ``out``, which receives dx).  With x, that of ``dispatch(x, routing, weighted=True)``: (dx,
+    dweights), dweights float32 [T, top_k] (ternary_dispatch_backward)."""
+    T, k = _check_routing(routing)
+    dt, N = _rows_of(grad, T * k, "grad")
+    _match(x, (T, N), grad.dtype, "x")
+    _match(add, (T, N), grad.dtype, "add")
+    dev = _same_device(grad, grad, routing.slots, routing.weights, x, add)
+    out = _output(out, (T, N), grad.dtype, dev, grad)
+    if out.dtype != grad.dtype:
+        raise ValueError("out must have grad's dtype")
+    dw = None if x is None else torch.empty_like(routing.weights)
+    _call("ternary_dispatch_backward", dev, grad.data_ptr(), dt, T * k, N, routing.slots.data_ptr(),
+          None if x is None else routing.weights.data_ptr(), T, k, _ptr(x), _ptr(add), out.data_ptr(), _ptr(dw))
+    return out if x is None else (out, dw)
+
+
+def combine_backward(grad: torch.Tensor, y: torch.Tensor, routing: Routing, out: torch.Tensor | None = None):
+    """The gradient of ``combine(y, routing)`` from grad [T, N], that of its result: (dy [T * top_k, N], dweights float32
+    [T, top_k]); that of its ``add`` is grad itself (ternary_combine_backward).  Rows of dy (``out``) at
+    places that hold no slot are not written."""
+    T, k = _check_routing(routing)
+    dt, N = _rows_of(grad, T, "grad")
+    _match(y, (T * k, N), grad.dtype, "y")
+    dev = _same_device(grad, grad, y, routing.slots, routing.weights)
+    out = _output(out, (T * k, N), grad.dtype, dev, grad)
+    if out.dtype != grad.dtype:
+        raise ValueError("out must have grad's dtype")
+    dw = torch.empty_like(routing.weights)
+    _call("ternary_combine_backward", dev, grad.data_ptr(), y.data_ptr(), dt, T * k, N, routing.slots.data_ptr(),
+          routing.weights.data_ptr(), T, k, out.data_ptr(), dw.data_ptr())
+    return out, dw
+
+
+def _check_adapters(x, a, b, routing, scale):
+    """Shapes of adapters' operands checked against each other -> dtype code, T, K, N, rank, E."""
+    dt = _ACT.get(x.dtype)
+    if dt is None or x.dim() != 2:
+        raise ValueError("x must be a 2-D bfloat16 or float16 tensor")
+    T, K = x.shape
+    if a.dim() != 3 or b.dim() != 3 or a.dtype != x.dtype or b.dtype != x.dtype or a.shape[2] != K \
+            or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+        raise ValueError(f"a [E, rank, {K}] and b [E, N, rank] must have x's dtype and share E and rank")
+    E, rank = a.shape[:2]
+    if scale is not None and (scale.dtype != torch.float32 or scale.shape != (E,)):
+        raise ValueError(f"scale must be a float32 tensor [{E}]")
+    if _check_routing(routing) != (T, 1) or routing.offsets.shape != (E + 1,):
+        raise ValueError(f"routing must be sort_slots() of {T} tokens' adapters, with {E + 1} offsets")
+    return dt, T, K, b.shape[1], rank, E
+
+
+def linear_adapters(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing,
+                    scale: torch.Tensor | None = None, add: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None, hidden: torch.Tensor | None = None) -> torch.Tensor:
+    """y [T, N] = add + scale[e] * (x @ a[e]^T) @ b[e]^T, e each token's adapter: low-rank adapters of many requests beside
+    a shared projection, whose output ``add`` is (and may be ``out``).  x [T, K], a [E, rank, K] and b
+    [E, N, rank] (rank up to 128; smaller ones filled up with zeros) share a dtype, bf16 or fp16; scale is float32
+    [E] (1 if not given); ``routing`` is ``sort_slots(adapters, E)``, made once for all projections of a batch.  A
+    token without an adapter gets ``add``, or 0.  ``hidden`` (float32 [T, rank]) receives x @ a[e]^T, for
+    linear_adapters_backward() (ternary_linear_adapters)."""
+    dt, T, K, N, rank, E = _check_adapters(x, a, b, routing, scale)
+    _match(add, (T, N), x.dtype, "add")
+    _match(hidden, (T, rank), torch.float32, "hidden")
+    dev = _same_device(x, x, a, b, scale, add, hidden, routing.offsets, routing.order, routing.slots)
+    out = _output(out, (T, N), x.dtype, dev, x)
+    if out.dtype != x.dtype:
+        raise ValueError("out must have x's dtype")
+    ws = _workspace("ternary_linear_adapters_workspace", x, T, K, N, rank, E)
+    _call("ternary_linear_adapters", dev, x.data_ptr(), dt, T, K, N, rank, a.data_ptr(), b.data_ptr(), E, _ptr(scale),
+          routing.offsets.data_ptr(), routing.order.data_ptr(), routing.slots.data_ptr(), _ptr(add), out.data_ptr(),
+          _ptr(hidden), _ptr(ws))
+    return out
+
+
+def linear_adapters_backward(grad: torch.Tensor, x: torch.Tensor, hidden: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                             routing: Routing, scale: torch.Tensor | None = None, add: torch.Tensor | None = None,
+                             out: torch.Tensor | None = None):
+    """The gradients of linear_adapters() from grad [T, N], that of its result: (dx [T, K], da, db), in x's dtype.
+    ``hidden`` is what the forward call wrote; ``add`` ([T, K], another gradient of x, such as the
+    projection's own; may be ``out``, which receives dx) is added to dx.  The gradient of the
+    forward call's ``add`` is grad itself (ternary_linear_adapters_backward)."""
+    dt, T, K, N, rank, E = _check_adapters(x, a, b, routing, scale)
+    _match(grad, (T, N), x.dtype, "grad")
+    _match(hidden, (T, rank), torch.float32, "hidden")
+    _match(add, (T, K), x.dtype, "add")
+    dev = _same_device(x, x, grad, hidden, a, b, scale, add, routing.offsets, routing.order, routing.slots)
+    out = _output(out, (T, K), x.dtype, dev, x)
+    if out.dtype != x.dtype:
+        raise ValueError("out must have x's dtype")
+    da, db = torch.empty_like(a), torch.empty_like(b)
+    ws = _workspace("ternary_linear_adapters_backward_workspace", x, T, K, N, rank, E)
+    _call("ternary_linear_adapters_backward", dev, grad.data_ptr(), x.data_ptr(), hidden.data_ptr(), dt, T, K, N, rank,
+          a.data_ptr(), b.data_ptr(), E, _ptr(scale), routing.offsets.data_ptr(), routing.order.data_ptr(),
+          routing.slots.data_ptr(), _ptr(add), out.data_ptr(), da.data_ptr(), db.data_ptr(), _ptr(ws))
+    return out, da, db
 
 
 # ---------------------------------------------------------------- probes

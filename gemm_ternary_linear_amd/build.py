@@ -25,7 +25,8 @@ FLAGS = [
 ]
 SOURCES = ["api.hip", "pack.hip", "gemv.hip", "gemv_f4.hip", "gemv_stream.hip", "gemv_valu.hip",
            "gemm_few.hip", "gemm.hip", "simple.hip", "noalloc.hip", "workspace.hip", "quantize.hip",
-           "api_fp8.hip", "fp8_quantize.hip", "fp8_products.hip", "route.hip", "combine.hip"]
+           "api_fp8.hip", "fp8_quantize.hip", "fp8_products.hip", "route.hip", "combine.hip",
+           "api_adapters.hip", "sort_slots.hip", "exchange.hip", "adapters.hip"]
 PROBE_SOURCES = ["probe.hip"]
 
 

@@ -1,0 +1,746 @@
+// Low-rank adapters beside a shared projection, each token with its own, and their gradients.
+// For a token t of adapter e (scale s, a [rank, K], b [N, rank]):
+//     v = x a^T,  y = add + s v b^T
+// and of a gradient g of y
+//     dv = s g b,  db = s sum_t g^T v,  da = sum_t dv^T x,  dx = add + dv a.
+//
+// Tokens come sorted by adapter (offsets, order), so a tile of neighbouring places shares its
+// weights.  Three kernels make up both directions:
+//     down  a long row times the weights: v and dv.  Split along the row over workgroups where the tiles are few;
+//           partial sums in fp32, added up in order by their readers.
+//     up    v times the weights, added to a row: y and dx.
+//     outer sums over an adapter's tokens: da and db.  Split into pieces of tokens; partial sums in fp32,
+//           added up in order by a fourth kernel where an adapter has several.
+// All products are on the matrix unit in 16 bits, their sums in fp32.  v and dv, which are fp32, enter it as
+// two 16-bit numbers, the nearest and the nearest to what that left: 2^-17 off (bf16; fp16 2^-22), far below the
+// outputs' own rounding, for twice the matrix cycles, of which there are plenty: the
+// layer is bound by reading x and reading and writing y.  fp16 would lose what is small or large, so there
+// v is first brought to below 2 by a power of two: a row's largest (up) or the piece's (outer).
+//
+// Operands that the matrix unit wants along the other axis than they lie in memory (b in down, a in up, both sides of
+// outer) pass through LDS and are read transposed (ds_read_b64_tr_b16: of 16 lanes, lane l gives the
+// address of four neighbours of row l / 4 at column 4 (l % 4), and receives column l of the four rows).
+#include "fp8_common.h"
+#include "internal.h"
+#include "places.h"
+#include "rows.h"
+
+namespace ternary {
+
+namespace {
+
+constexpr int kWaves = 4, kThreads = kWaves * 64;
+constexpr int kUpRows = 64;    // places of an up tile
+constexpr int kCols = 256;     // columns of an up or outer workgroup: 64 a wave
+constexpr int kStep = 32;      // tokens of a step of outer
+
+template <int DT>
+__device__ __forceinline__ f32x4_t mfma(u32x4_v a, u32x4_v b, f32x4_t c)
+{
+    if constexpr (DT == TERNARY_FP16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+typedef short s16x4_v __attribute__((ext_vector_type(4)));
+
+// Eight rows (from the lane group's first) of the column that the lane takes, transposed: `p` is the address of row
+// l / 4, column 4 (l % 4) of the group's rows, `ld` elements between rows.
+__device__ __forceinline__ u32x4_v read_transposed(const uint16_t *p, int ld)
+{
+#if defined(__HIP_DEVICE_COMPILE__)
+    typedef __attribute__((address_space(3))) s16x4_v lds_s4;
+    const s16x4_v lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)p);
+    const s16x4_v hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4 *)(p + 4 * ld));
+    const u32x2_v l = __builtin_bit_cast(u32x2_v, lo), h = __builtin_bit_cast(u32x2_v, hi);
+    return u32x4_v{l.x, l.y, h.x, h.y};
+#else
+    return u32x4_v{};
+#endif
+}
+
+// Elements i .. i + 7 of a row of n that starts at p; 0 past its end.
+template <bool WIDE>
+__device__ __forceinline__ u32x4_v row_piece(const uint16_t *p, int i, int n)
+{
+    return load_piece<TERNARY_BF16, WIDE>(p, i, n - i).d[0];
+}
+
+// v as two 16-bit numbers (bits): the nearest, and the nearest to the rest.
+template <int DT>
+__device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo)
+{
+    constexpr bool H = DT == TERNARY_FP16;
+    float h;
+    if constexpr (H) {
+        hi = f32_to_f16_rne(v);
+        h = f16_bits_to_f32(hi);
+    } else {
+        hi = f32_to_bf16_rne(v);
+        if ((hi & 0x7fff) == 0x7f80 && fabsf(v) < INFINITY)
+            hi -= 1;  // (the largest, where rounding went past it)
+        h = __builtin_bit_cast(float, (uint32_t)hi << 16);
+    }
+    lo = fabsf(v) == INFINITY ? (uint16_t)0 : round_out<H>(v - h);
+}
+
+// fp32 rows [T, rank] held as `parts` partial sums, `stride` elements apart.
+struct Small {
+    const float *p;
+    int parts, rank;
+    int64_t stride;
+};
+__device__ __forceinline__ void load_small(const Small &s, int64_t t, int j0, float v[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = 0.f;
+    const float *p = s.p + t * s.rank + j0;
+    for (int k = 0; k < s.parts; ++k, p += s.stride) {
+        if (s.rank % 4 == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (j0 + 4 * h < s.rank) {
+                    const f32x4_t u = *reinterpret_cast<const f32x4_t *>(p + 4 * h);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[4 * h + i] += u[i];
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] += j0 + i < s.rank ? p[i] : 0.f;
+        }
+    }
+}
+
+// The exponent that brings the largest finite |v[i]| to 1 .. 2 (0 where all are 0).
+__device__ __forceinline__ float largest(const float v[8])
+{
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        m = fmaxf(m, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.f);
+    return m;
+}
+__device__ __forceinline__ int exponent(float m) { return m > 0.f ? ilogbf(m) : 0; }
+
+// Eight values, times 2^-ex, split, into a row of LDS: [hi: RP][lo: RP].
+template <int DT, int RP>
+__device__ __forceinline__ void put_split(uint16_t *row, int j0, const float v[8], int ex)
+{
+    uint16_t hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        split<DT>(DT == TERNARY_FP16 ? ldexpf(v[i], -ex) : v[i], hi[i], lo[i]);
+    u32x4_v h, l;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = (uint32_t)hi[2 * i] | (uint32_t)hi[2 * i + 1] << 16;
+        l[i] = (uint32_t)lo[2 * i] | (uint32_t)lo[2 * i + 1] << 16;
+    }
+    *reinterpret_cast<u32x4_v *>(row + j0) = h;
+    *reinterpret_cast<u32x4_v *>(row + RP + j0) = l;
+}
+
+// The token at place p, or -1.
+__device__ __forceinline__ int token_at(const int32_t *order, int p, int end, int T)
+{
+    const int t = p < end ? order[p] : -1;
+    return t < T ? t : -1;
+}
+
+// ---------------------------------------------------------------- down
+
+struct DownArgs {
+    const uint16_t *x, *w;  // [T, L]; [E, rank, L], or (TR) [E, L, rank]
+    const float *scale;
+    const int32_t *offsets, *order;
+    float *out;  // [splits][T, rank]
+    int T, L, rank, E, splits;
+};
+
+// A workgroup takes 16 MF places and a share of the row; its waves take turns at 64 elements of it (whole
+// cache lines) and meet at the end.
+template <int DT, int RF, int MF, bool TR, bool WIDE>
+__global__ void __launch_bounds__(kThreads) down_kernel(const DownArgs a)
+{
+    constexpr int RP = RF * 16, LD = RP + 8;
+    constexpr int STAGE = TR ? kWaves * 64 * LD * 2 : 0, SUMS = kWaves * MF * 64 * 16;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[STAGE > SUMS ? STAGE : SUMS];
+    const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile = blockIdx.x / a.splits, part = blockIdx.x - tile * a.splits;
+    int e, r0, r1;
+    if (!find_tile<16 * MF>(a.offsets, a.E, a.T, tile, e, r0, r1))
+        return;
+    int tok[MF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+        tok[m] = token_at(a.order, r0 + m * 16 + col, r1, a.T);
+    f32x4_t acc[RF][MF] = {};
+    const int steps = (a.L + 63) / 64;
+    const int lo = (int)((int64_t)steps * part / a.splits), hi = (int)((int64_t)steps * (part + 1) / a.splits);
+    const uint16_t *w = a.w + (int64_t)e * a.rank * a.L;
+    uint16_t *stage = reinterpret_cast<uint16_t *>(lds) + wave * 64 * LD;
+    for (int i = lo + wave; i < hi; i += kWaves) {
+        const int k0 = i * 64;
+        u32x4_v xf[2][MF], wf[2][RF];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+                xf[h][m] = tok[m] >= 0 ? row_piece<WIDE>(a.x + (int64_t)tok[m] * a.L, k0 + h * 32 + g * 8, a.L) : u32x4_v{};
+        if constexpr (TR) {
+            constexpr int PER = RP / 8;  // pieces of a row
+#pragma unroll
+            for (int q = 0; q < PER; ++q) {
+                const int row = (lane + q * 64) / PER, j = (lane + q * 64) % PER * 8;
+                const u32x4_v v = k0 + row < a.L ? row_piece<WIDE>(w + (int64_t)(k0 + row) * a.rank, j, a.rank) : u32x4_v{};
+                *reinterpret_cast<u32x4_v *>(stage + row * LD + j) = v;
+            }
+            asm volatile("" ::: "memory");  // (a wave's LDS accesses are in order)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int f = 0; f < RF; ++f)
+                    wf[h][f] = read_transposed(stage + (h * 32 + g * 8 + col / 4) * LD + f * 16 + col % 4 * 4, LD);
+            asm volatile("" ::: "memory");
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int f = 0; f < RF; ++f) {
+                    const int j = f * 16 + col;
+                    wf[h][f] = j < a.rank ? row_piece<WIDE>(w + (int64_t)j * a.L, k0 + h * 32 + g * 8, a.L) : u32x4_v{};
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int f = 0; f < RF; ++f)
+#pragma unroll
+                for (int m = 0; m < MF; ++m)
+                    acc[f][m] = mfma<DT>(wf[h][f], xf[h][m], acc[f][m]);
+    }
+    // the waves' sums, 16 of the rank at a time
+    f32x4_t *sums = reinterpret_cast<f32x4_t *>(lds);
+    const float s = a.scale ? a.scale[e] : 1.f;
+    float *out = a.out + (int64_t)part * a.T * a.rank;
+#pragma unroll
+    for (int f = 0; f < RF; ++f) {
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+            sums[(wave * MF + m) * 64 + lane] = acc[f][m];
+        __syncthreads();
+        for (int m = wave; m < MF; m += kWaves) {
+            f32x4_t v = sums[m * 64 + lane];
+#pragma unroll
+            for (int u = 1; u < kWaves; ++u)
+                v += sums[(u * MF + m) * 64 + lane];
+            const int t = token_at(a.order, r0 + m * 16 + col, r1, a.T), j = f * 16 + g * 4;
+            if (t >= 0) {
+                if (a.rank % 4 == 0) {
+                    if (j < a.rank)
+                        *reinterpret_cast<f32x4_t *>(out + (int64_t)t * a.rank + j) = v * s;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (j + i < a.rank)
+                            out[(int64_t)t * a.rank + j + i] = v[i] * s;
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- up
+
+struct UpArgs {
+    Small v;
+    const uint16_t *w;  // [E, C, rank], or (TR) [E, rank, C]
+    const float *scale;
+    const int32_t *offsets, *order, *slots;
+    const uint16_t *add;
+    uint16_t *y;
+    float *hidden;  // v's sums are written here, or NULL
+    int T, C, rank, E;
+    int chunks, per;  // runs of 256 columns; how many a workgroup takes
+};
+
+// A wave takes 64 columns: rows of the matrix operand in an order that leaves a lane with 16 neighbouring columns of
+// a token.  Its weights stay in registers while the tile's places pass.
+template <int DT, int RF, bool TR, bool WIDE>
+__global__ void __launch_bounds__(kThreads) up_kernel(const UpArgs a)
+{
+    constexpr int RP = RF * 16, LDV = 2 * RP + 8, LDW = kCols + 16;
+    constexpr int QW = RP < 32 ? 1 : RP / 32, Q = 2 * RP / 32;  // operands of the weights, and of v
+    __shared__ __attribute__((aligned(16))) uint16_t sv[kUpRows * LDV];
+    __shared__ __attribute__((aligned(16))) uint16_t sw[TR ? RP * LDW : 8];
+    __shared__ float factor[kUpRows];
+    __shared__ int toks[kUpRows];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int runs = (a.chunks + a.per - 1) / a.per;
+    const int tile = blockIdx.x / runs, run = blockIdx.x - tile * runs;
+    const int c0 = run * a.per, c1 = min(a.chunks, c0 + a.per);
+    // tokens without an adapter, 64 of them looked at by each tile
+    if (a.y != a.add && (int64_t)tile * kUpRows < a.T)
+        for (int row = tid / 32; row < kUpRows; row += kThreads / 32) {
+            const int64_t t = (int64_t)tile * kUpRows + row;
+            if (t >= a.T || (unsigned)a.slots[t] < (unsigned)a.T)
+                continue;
+            for (int n = c0 * kCols + tid % 32 * 8; n < min(c1 * kCols, a.C); n += kCols) {
+                Raw<DT> v = {};
+                if (a.add)
+                    v = load_piece<DT, WIDE>(a.add, t * a.C + n, a.C - n);
+                store_piece<DT, WIDE>(a.y, t * a.C + n, a.C - n, v);
+            }
+        }
+    int e, r0, r1;
+    if (!find_tile<kUpRows>(a.offsets, a.E, a.T, tile, e, r0, r1))
+        return;
+    const float s = a.scale ? a.scale[e] : 1.f;
+    // v, in 16-bit halves; RP / 8 threads a row
+    constexpr int PER = RP / 8;
+#pragma unroll
+    for (int base = 0; base < kUpRows * PER; base += kThreads) {
+        const int i = base + tid, row = i / PER, j0 = i % PER * 8;
+        if (kUpRows * PER % kThreads != 0 && row >= kUpRows)
+            break;
+        const int t = token_at(a.order, r0 + row, r1, a.T);
+        float v[8] = {};
+        if (t >= 0) {
+            load_small(a.v, t, j0, v);
+            if (a.hidden && run == 0)
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (j0 + k < a.rank)
+                        a.hidden[(int64_t)t * a.rank + j0 + k] = v[k];
+        }
+        int ex = 0;
+        if constexpr (DT == TERNARY_FP16) {
+            float m = largest(v);
+#pragma unroll
+            for (int o = 1; o < PER; o <<= 1)
+                m = fmaxf(m, __shfl_xor(m, o));
+            ex = exponent(m);
+        }
+        put_split<DT, RP>(sv + row * LDV, j0, v, ex);
+        if (j0 == 0)
+            factor[row] = ldexpf(s, ex), toks[row] = t;
+    }
+    const uint16_t *w = a.w + (int64_t)e * a.rank * a.C;
+    for (int c = c0; c < c1; ++c) {
+        const int n0 = c * kCols + wave * 64;  // this wave's columns
+        u32x4_v wf[4][QW];
+        if constexpr (TR) {
+            __syncthreads();
+#pragma unroll
+            for (int base = 0; base < RP * 32; base += kThreads) {
+                const int row = (base + tid) / 32, n = tid % 32 * 8;
+                const u32x4_v v = row < a.rank ? row_piece<WIDE>(w + (int64_t)row * a.C, c * kCols + n, a.C) : u32x4_v{};
+                *reinterpret_cast<u32x4_v *>(sw + row * LDW + n) = v;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+                for (int q = 0; q < QW; ++q) {
+                    // lane group g: rows 8 g on of 32; of a rank of 16 they are there twice (v's halves)
+                    const int j = RP < 32 ? (g & 1) * 8 : q * 32 + g * 8;
+                    wf[f][q] = read_transposed(sw + (j + col / 4) * LDW + wave * 64 + col % 4 * 16 + f * 4, LDW);
+                }
+        } else {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const int n = n0 + col / 4 * 16 + f * 4 + col % 4;
+#pragma unroll
+                for (int q = 0; q < QW; ++q) {
+                    const int j = RP < 32 ? (g & 1) * 8 : q * 32 + g * 8;
+                    wf[f][q] = n < a.C ? row_piece<WIDE>(w + (int64_t)n * a.rank, j, a.rank) : u32x4_v{};
+                }
+            }
+            if (c == c0)
+                __syncthreads();
+        }
+        const int n = n0 + g * 16;
+#pragma unroll
+        for (int m = 0; m < kUpRows / 16; ++m) {
+            if (r0 + m * 16 >= r1)
+                break;
+            const int row = m * 16 + col, t = toks[row];
+            Raw<DT> base[2] = {};
+            if (a.add && t >= 0)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (n + h * 8 < a.C)
+                        base[h] = load_piece<DT, WIDE>(a.add, (int64_t)t * a.C + n + h * 8, a.C - n - h * 8);
+            f32x4_t acc[4] = {};
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const u32x4_v vf = *reinterpret_cast<const u32x4_v *>(sv + row * LDV + q * 32 + g * 8);
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                    acc[f] = mfma<DT>(wf[f][q % QW], vf, acc[f]);
+            }
+            const float by = factor[row];
+            if (t >= 0)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (n + h * 8 < a.C) {
+                        float o[8];
+                        widen_piece(base[h], o);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            o[i] += by * acc[2 * h + i / 4][i % 4];
+                        store_piece<DT, WIDE>(a.y, (int64_t)t * a.C + n + h * 8, a.C - n - h * 8, round_piece<DT>(o));
+                    }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- outer
+
+struct OuterProblem {
+    const uint16_t *d;  // [T, C]
+    Small v;
+    uint16_t *out;
+    float *partial;     // [pieces of adapters with several][rank * C]
+    const float *scale;
+    int C, chunks;
+};
+struct OuterArgs {
+    OuterProblem p[2];  // out [E, C, rank]; out [E, rank, C]
+    const int32_t *offsets, *order;
+    int T, rank, E;
+    int piece, partials;  // tokens of a piece; pieces that `partial` has room for
+};
+
+// A workgroup takes a piece of an adapter's tokens and 256 columns, 64 a wave.  Steps of 32 tokens pass through LDS
+// as they lie, and both operands are read transposed; the next step's loads are under way meanwhile.
+// BY_RANK: the output is [E, rank, C], else [E, C, rank].
+template <int DT, int RF, bool WIDE, bool BY_RANK>
+__device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProblem &p, int idx, int c0, uint16_t *sd,
+                                            uint16_t *sv, float *most)
+{
+    constexpr int RP = RF * 16, LDV = 2 * RP + 8, LDD = kCols + 16;
+    constexpr int PER = RP / 8, NV = (kStep * PER + kThreads - 1) / kThreads, ND = kStep * 32 / kThreads;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    int e, r0, r1, pieces, number;
+    if (!find_piece(a.offsets, a.E, a.T, a.piece, idx, e, r0, r1, pieces, number) || (pieces > 1 && number >= a.partials))
+        return;
+    int ex = 0;
+    if constexpr (DT == TERNARY_FP16) {
+        float m = 0.f;
+        for (int i = tid; i < (r1 - r0) * PER; i += kThreads) {
+            const int t = token_at(a.order, r0 + i / PER, r1, a.T);
+            float v[8];
+            if (t >= 0 && i % PER * 8 < a.rank) {
+                load_small(p.v, t, i % PER * 8, v);
+                m = fmaxf(m, largest(v));
+            }
+        }
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1)
+            m = fmaxf(m, __shfl_xor(m, o));
+        if (lane == 0)
+            most[wave] = m;
+        __syncthreads();
+        ex = exponent(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])));
+    }
+    u32x4_v nd[ND];
+    float nv[NV][8];
+    auto fetch = [&](int r) {
+#pragma unroll
+        for (int q = 0; q < ND; ++q) {
+            const int row = (tid + q * kThreads) / 32, n = c0 + tid % 32 * 8;
+            const int t = token_at(a.order, r + row, r1, a.T);
+            nd[q] = t >= 0 ? row_piece<WIDE>(p.d + (int64_t)t * p.C, n, p.C) : u32x4_v{};
+        }
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            const int i = tid + q * kThreads;
+            const int t = i / PER < kStep ? token_at(a.order, r + i / PER, r1, a.T) : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                nv[q][k] = 0.f;
+            if (t >= 0)
+                load_small(p.v, t, i % PER * 8, nv[q]);
+        }
+    };
+    f32x4_t acc[4][RF] = {};
+    fetch(r0);
+    for (int r = r0; r < r1; r += kStep) {
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < ND; ++q)
+            *reinterpret_cast<u32x4_v *>(sd + (tid + q * kThreads) / 32 * LDD + tid % 32 * 8) = nd[q];
+#pragma unroll
+        for (int q = 0; q < NV; ++q) {
+            const int i = tid + q * kThreads;
+            if (i / PER < kStep)
+                put_split<DT, RP>(sv + i / PER * LDV, i % PER * 8, nv[q], ex);
+        }
+        __syncthreads();
+        if (r + kStep < r1)
+            fetch(r + kStep);
+        u32x4_v df[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            df[c] = read_transposed(sd + (g * 8 + col / 4) * LDD + wave * 64 + c * 16 + col % 4 * 4, LDD);
+#pragma unroll
+        for (int f = 0; f < RF; ++f)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const u32x4_v vf = read_transposed(sv + (g * 8 + col / 4) * LDV + h * RP + f * 16 + col % 4 * 4, LDV);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    acc[c][f] = BY_RANK ? mfma<DT>(df[c], vf, acc[c][f]) : mfma<DT>(vf, df[c], acc[c][f]);
+            }
+    }
+    const int64_t size = (int64_t)a.rank * p.C;
+    const float by = ldexpf(p.scale ? p.scale[e] : 1.f, ex);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int f = 0; f < RF; ++f) {
+            // four neighbours of the axis that lies contiguous in the output
+            const int j = f * 16 + (BY_RANK ? col : g * 4), n = c0 + wave * 64 + c * 16 + (BY_RANK ? g * 4 : col);
+            const int64_t i = BY_RANK ? (int64_t)j * p.C + n : (int64_t)n * a.rank + j;
+            const int left = BY_RANK ? (j < a.rank ? p.C - n : 0) : (n < p.C ? a.rank - j : 0);
+            const int len = BY_RANK ? p.C : a.rank;
+            if (left <= 0)
+                continue;
+            const f32x4_t v = acc[c][f] * by;
+            if (pieces > 1) {
+                float *o = p.partial + number * size + i;
+                if (len % 4 == 0)
+                    *reinterpret_cast<f32x4_t *>(o) = v;
+                else
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < left)
+                            o[k] = v[k];
+            } else {
+                uint16_t *o = p.out + e * size + i;
+                if (len % 4 == 0)
+                    store4<DT>(o, 0, v);
+                else
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < left)
+                            store_elem<DT>(o, k, v[k]);
+            }
+        }
+}
+
+template <int DT, int RF, bool WIDE>
+__global__ void __launch_bounds__(kThreads) outer_kernel(const OuterArgs a)
+{
+    __shared__ __attribute__((aligned(16))) uint16_t sd[kStep * (kCols + 16)], sv[kStep * (RF * 32 + 8)];
+    __shared__ float most[kWaves];
+    const int chunks = a.p[0].chunks + a.p[1].chunks, idx = blockIdx.x / chunks, at = blockIdx.x - idx * chunks;
+    if (at < a.p[0].chunks)
+        outer_piece<DT, RF, WIDE, false>(a, a.p[0], idx, at * kCols, sd, sv, most);
+    else
+        outer_piece<DT, RF, WIDE, true>(a, a.p[1], idx, (at - a.p[0].chunks) * kCols, sd, sv, most);
+}
+
+// Gradients of adapters with several pieces, and zeros for those without tokens: four neighbours a thread.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) outer_sum_kernel(const OuterArgs a, int blocks0)
+{
+    const int which = (int)blockIdx.x >= blocks0, e = blockIdx.y;
+    const OuterProblem &p = a.p[which];
+    int pieces, first;
+    expert_pieces(a.offsets, a.E, a.T, a.piece, e, pieces, first);
+    if (pieces == 1)
+        return;
+    pieces = min(pieces, a.partials - first);
+    const int64_t size = (int64_t)a.rank * p.C;
+    const int64_t i = ((int64_t)(blockIdx.x - (which ? blocks0 : 0)) * kThreads + threadIdx.x) * 4;
+    if (i >= size)
+        return;
+    float v[4] = {};
+    uint16_t *o = p.out + e * size + i;
+    if (size % 4 == 0) {
+#pragma unroll 4
+        for (int k = 0; k < pieces; ++k) {
+            const f32x4_t u = *reinterpret_cast<const f32x4_t *>(p.partial + (first + k) * size + i);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] += u[q];
+        }
+        store4<DT>(o, 0, f32x4_t{v[0], v[1], v[2], v[3]});
+    } else {
+        for (int k = 0; k < pieces; ++k)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                v[q] += i + q < size ? p.partial[(first + k) * size + i + q] : 0.f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            if (i + q < size)
+                store_elem<DT>(o, q, v[q]);
+    }
+}
+
+// ---------------------------------------------------------------- launches
+
+inline int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m; }
+// Tiles of `rows` places that T places of E adapters may need.
+inline int64_t tiles_of(int64_t T, int64_t E, int64_t rows) { return T / rows + (E < T ? E : T); }
+inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+
+// Fragments of 16 tokens of a down tile.
+inline int down_rows(int64_t T, int64_t E, int64_t rank) { return T <= 16 * E ? 1 : rank > 64 ? 2 : 4; }
+inline int down_splits(int64_t T, int64_t E, int64_t L, int64_t rank)
+{
+    const int64_t tiles = up_to(T, 16 * down_rows(T, E, rank)) + (E < T ? E : T) / 2, steps = up_to(L, 256);
+    const int64_t want = up_to(512, tiles > 0 ? tiles : 1);
+    return (int)(want < steps ? want : steps);
+}
+inline int piece_tokens(int64_t T, int64_t K, int64_t N)
+{
+    const int64_t chunks = up_to(K, kCols) + up_to(N, kCols), want = T * chunks / 1024 / kStep * kStep;
+    return (int)(want < 128 ? 128 : want > 1024 ? 1024 : want);
+}
+inline int64_t round256(int64_t n) { return (n + 255) & ~(int64_t)255; }
+inline int64_t small_bytes(int64_t T, int64_t E, int64_t L, int64_t rank)
+{
+    return round256(T * rank * 4 * down_splits(T, E, L, rank));
+}
+
+// Runs f(dtype, fragments of 16 of the rank, wide rows) as compile-time values.
+template <class F>
+void with_rank(bool fp16, int rank, bool wide, F f)
+{
+    auto by_type = [&](auto dt) {
+        auto by_width = [&](auto rf) {
+            if (wide)
+                f(dt, rf, std::true_type());
+            else
+                f(dt, rf, std::false_type());
+        };
+        if (rank <= 16)
+            by_width(std::integral_constant<int, 1>());
+        else if (rank <= 32)
+            by_width(std::integral_constant<int, 2>());
+        else if (rank <= 64)
+            by_width(std::integral_constant<int, 4>());
+        else
+            by_width(std::integral_constant<int, 8>());
+    };
+    if (fp16)
+        by_type(std::integral_constant<int, TERNARY_FP16>());
+    else
+        by_type(std::integral_constant<int, TERNARY_BF16>());
+}
+
+template <bool TR>
+hipError_t launch_down(const DownArgs &d, bool fp16, hipStream_t stream)
+{
+    const int mf = down_rows(d.T, d.E, d.rank);
+    const bool wide = d.L % 8 == 0 && aligned16(d.x) && aligned16(d.w) && (!TR || d.rank % 8 == 0);
+    const dim3 grid((unsigned)(tiles_of(d.T, d.E, 16 * mf) * d.splits));
+    with_rank(fp16, d.rank, wide, [&](auto dt, auto rf, auto wd) {
+        constexpr int DT = decltype(dt)::value, RF = decltype(rf)::value;
+        constexpr bool WIDE = decltype(wd)::value;
+        if (mf == 1)
+            hipLaunchKernelGGL((down_kernel<DT, RF, 1, TR, WIDE>), grid, dim3(kThreads), 0, stream, d);
+        else
+            hipLaunchKernelGGL((down_kernel<DT, RF, (RF > 4 ? 2 : 4), TR, WIDE>), grid, dim3(kThreads), 0, stream, d);
+    });
+    return hipGetLastError();
+}
+
+template <bool TR>
+hipError_t launch_up(UpArgs u, bool fp16, hipStream_t stream)
+{
+    u.chunks = (int)up_to(u.C, kCols);
+    const int64_t tiles = tiles_of(u.T, u.E, kUpRows);
+    const int64_t per = tiles * u.chunks / 2048;
+    u.per = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+    const bool wide = u.C % 8 == 0 && aligned16(u.w) && aligned16(u.add) && aligned16(u.y) && (TR || u.rank % 8 == 0);
+    const dim3 grid((unsigned)(tiles * up_to(u.chunks, u.per)));
+    with_rank(fp16, u.rank, wide, [&](auto dt, auto rf, auto wd) {
+        hipLaunchKernelGGL((up_kernel<decltype(dt)::value, decltype(rf)::value, TR, decltype(wd)::value>), grid,
+                           dim3(kThreads), 0, stream, u);
+    });
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t adapters_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E)
+{
+    (void)N;
+    return small_bytes(T, E, K, rank);
+}
+
+int64_t adapters_back_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E)
+{
+    const int64_t partials = 2 * T / piece_tokens(T, K, N);
+    return small_bytes(T, E, N, rank) + round256(partials * rank * N * 4) + round256(partials * rank * K * 4);
+}
+
+hipError_t launch_adapters(const AdapterArgs &a, hipStream_t stream)
+{
+    const int splits = down_splits(a.T, a.E, a.K, a.rank);
+    float *v = static_cast<float *>(a.workspace);
+    const DownArgs d = {a.x, a.a, nullptr, a.offsets, a.order, v, a.T, a.K, a.rank, a.E, splits};
+    hipError_t e = launch_down<false>(d, a.fp16, stream);
+    if (e != hipSuccess)
+        return e;
+    const UpArgs u = {{v, splits, a.rank, (int64_t)a.T * a.rank}, a.b, a.scale, a.offsets, a.order, a.slots, a.add, a.y,
+                      a.hidden, a.T, a.N, a.rank, a.E, 0, 0};
+    return launch_up<false>(u, a.fp16, stream);
+}
+
+hipError_t launch_adapters_back(const AdapterArgs &a, hipStream_t stream)
+{
+    const int piece = piece_tokens(a.T, a.K, a.N), splits = down_splits(a.T, a.E, a.N, a.rank);
+    const int partials = (int)(2 * (int64_t)a.T / piece);
+    char *ws = static_cast<char *>(a.workspace);
+    float *dv = reinterpret_cast<float *>(ws);
+    ws += small_bytes(a.T, a.E, a.N, a.rank);
+    float *part_b = reinterpret_cast<float *>(ws);
+    ws += round256((int64_t)partials * a.rank * a.N * 4);
+    float *part_a = reinterpret_cast<float *>(ws);
+    const Small small = {dv, splits, a.rank, (int64_t)a.T * a.rank};
+    hipError_t e = hipSuccess;
+    const OuterArgs o = {{{a.grad, {a.hidden, 1, a.rank, 0}, a.db, part_b, a.scale, a.N, (int)up_to(a.N, kCols)},
+                          {a.x, small, a.da, part_a, nullptr, a.K, (int)up_to(a.K, kCols)}},
+                         a.offsets, a.order, a.T, a.rank, a.E, piece, partials};
+    if (a.T) {
+        const DownArgs d = {a.grad, a.b, a.scale, a.offsets, a.order, dv, a.T, a.N, a.rank, a.E, splits};
+        e = launch_down<true>(d, a.fp16, stream);
+        if (e != hipSuccess)
+            return e;
+        const bool wide = a.N % 8 == 0 && a.K % 8 == 0 && aligned16(a.grad) && aligned16(a.x);
+        const dim3 grid((unsigned)(tiles_of(a.T, a.E, piece) * (o.p[0].chunks + o.p[1].chunks)));
+        with_rank(a.fp16, a.rank, wide, [&](auto dt, auto rf, auto wd) {
+            hipLaunchKernelGGL((outer_kernel<decltype(dt)::value, decltype(rf)::value, decltype(wd)::value>), grid,
+                               dim3(kThreads), 0, stream, o);
+        });
+        e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+        const UpArgs u = {small, a.a, nullptr, a.offsets, a.order, a.slots, a.add, a.dx, nullptr, a.T, a.K, a.rank, a.E, 0, 0};
+        e = launch_up<true>(u, a.fp16, stream);
+        if (e != hipSuccess)
+            return e;
+    }
+    const int blocks0 = (int)up_to((int64_t)a.rank * a.N, kThreads * 4), blocks1 = (int)up_to((int64_t)a.rank * a.K, kThreads * 4);
+    const dim3 grid((unsigned)(blocks0 + blocks1), (unsigned)a.E);
+    if (a.fp16)
+        hipLaunchKernelGGL((outer_sum_kernel<TERNARY_FP16>), grid, dim3(kThreads), 0, stream, o, blocks0);
+    else
+        hipLaunchKernelGGL((outer_sum_kernel<TERNARY_BF16>), grid, dim3(kThreads), 0, stream, o, blocks0);
+    return hipGetLastError();
+}
+
+}  // namespace ternary

@@ -19,6 +19,7 @@
 // same ones: of 8-bit weights k = 16 g .. and 64 + 16 g .. (16 each) in lane group g (lanes 16 g up).
 #include "fp8_common.h"
 #include "internal.h"
+#include "places.h"
 
 namespace ternary {
 
@@ -72,72 +73,6 @@ constexpr int second_chunk(bool tern) { return tern ? 1 : 4; }
 
 // Scale of a channel's fp4 products.
 __device__ __forceinline__ float channel_scale(uint16_t s) { return 0.5f * f16_bits_to_f32(s); }
-
-// Inclusive sum over the lanes of a wave (row shifts, then each row's total to
-// the rows after it).
-__device__ __forceinline__ int wave_scan(int v)
-{
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15, 31
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);
-    return v;
-}
-
-// Places [r0, r1) of expert e that the idx-th tile of BM rows covers (tiles run
-// expert by expert); false past the last.  Every lane of a wave calls it; lane l
-// looks at experts EP l .. EP l + EP - 1.  Whatever the offsets hold, the places are within
-// [0, R) and the expert within [0, E).
-template <int BM, int EP>
-__device__ __forceinline__ bool find_tile_of(const int32_t *offsets, int E, int R, int idx, int &e,
-                                             int &r0, int &r1)
-{
-    const int lo = (threadIdx.x & 63) * EP;
-    int o[EP + 1];
-#pragma unroll
-    for (int i = 0; i <= EP; ++i)
-        o[i] = offsets[min(lo + i, E)];
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < EP; ++i) {
-        const int a = max(o[i], 0), b = min(o[i + 1], R);
-        mine += b > a ? (b - a + BM - 1) / BM : 0;
-    }
-    const int incl = wave_scan(mine);
-    int left = idx - (incl - mine), fe = -1, f0 = 0, f1 = 0;
-    const uint64_t here = __builtin_amdgcn_ballot_w64(left >= 0 && left < mine);
-    if (!here)
-        return false;
-#pragma unroll
-    for (int i = 0; i < EP; ++i) {
-        const int a = max(o[i], 0), b = min(o[i + 1], R);
-        const int tiles = b > a ? (b - a + BM - 1) / BM : 0;
-        if (left >= 0 && left < tiles) {
-            fe = lo + i;
-            f0 = a + left * BM;
-            f1 = min(b, f0 + BM);
-        }
-        left -= tiles;
-    }
-    const int from = __builtin_ctzll(here);
-    e = __builtin_amdgcn_readlane(fe, from);
-    r0 = __builtin_amdgcn_readlane(f0, from);
-    r1 = __builtin_amdgcn_readlane(f1, from);
-    return e >= 0;
-}
-
-template <int BM>
-__device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int R, int idx, int &e,
-                                          int &r0, int &r1)
-{
-    if (E <= 64)
-        return find_tile_of<BM, 1>(offsets, E, R, idx, e, r0, r1);
-    if (E <= 256)
-        return find_tile_of<BM, 4>(offsets, E, R, idx, e, r0, r1);
-    return find_tile_of<BM, 8>(offsets, E, R, idx, e, r0, r1);
-}
 
 // 16 codes (one word) -> the fp4 words of its odd and of its even codes (the
 // field (b1 b0) becomes (sign, magnitude) = (b1, b0 ^ b1) at a nibble's top).

@@ -234,4 +234,48 @@ struct CombineArgs {
 };
 hipError_t launch_combine(const CombineArgs &a, int dtype, hipStream_t stream);
 
+// ---------------------------------------------------------------- slots of given indices, the exchange's gradients
+
+struct SortArgs {
+    const int32_t *ids;
+    float *ones;  // or NULL
+    int32_t *offsets, *order, *slots, *counts;
+    int64_t n;  // slots
+    int E;
+};
+int64_t sort_slots_workspace(int64_t n, int64_t E);
+hipError_t launch_sort_slots(const SortArgs &a, hipStream_t stream);
+
+struct ExchangeArgs {
+    const void *x;     // dispatch, its gradient: tokens [T, N]; combine's gradient: rows [R, N]
+    const void *grad;  // dispatch's gradient: rows [R, N]; combine's: tokens
+    const void *add;
+    void *out;
+    const int32_t *slots;
+    const float *weights;
+    float *dweights;
+    int64_t T, R;
+    int N, k;
+};
+hipError_t launch_dispatch(const ExchangeArgs &a, int dtype, hipStream_t stream);
+hipError_t launch_combine_back(const ExchangeArgs &a, int dtype, hipStream_t stream);
+hipError_t launch_dispatch_back(const ExchangeArgs &a, int dtype, hipStream_t stream);
+
+// ---------------------------------------------------------------- low-rank adapters
+
+struct AdapterArgs {
+    const uint16_t *x, *a, *b, *grad, *add;  // [T, K], [E, rank, K], [E, N, rank], [T, N], [T, N] or [T, K]
+    const float *scale;                      // [E], or NULL for 1
+    const int32_t *offsets, *order, *slots;
+    uint16_t *y, *dx, *da, *db;
+    float *hidden;  // [T, rank]: written by the layer where not NULL, read by its gradient
+    void *workspace;
+    int T, K, N, rank, E;
+    bool fp16;
+};
+int64_t adapters_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E);
+int64_t adapters_back_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E);
+hipError_t launch_adapters(const AdapterArgs &a, hipStream_t stream);
+hipError_t launch_adapters_back(const AdapterArgs &a, hipStream_t stream);
+
 }  // namespace ternary

@@ -521,6 +521,134 @@ int ternary_combine(const void *y, int dtype, int64_t R, int64_t N, const int32_
                     const float *weights, int64_t T, int top_k, const void *add, void *out,
                     hipStream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Training beside frozen ternary weights, and many adapters at once.  Slots sorted by given indices (another
+ * router's experts, or each token's adapter), rows sent to their places and the gradients
+ * of that exchange, and low-rank adapters beside a shared projection with their gradients:
+ *
+ *   ids -> ternary_sort_slots -> offsets, order, slots
+ *   x   -> ternary_dispatch -> the experts -> ternary_combine, and back:
+ *          ternary_combine_backward -> the experts' gradients -> ternary_dispatch_backward
+ *   y = x W^T -> ternary_linear_adapters (add = y) -> ternary_linear_adapters_backward
+ *
+ * The conventions above hold; none of these uses a workspace of the library, so any of them
+ * may be captured, replayed and run on several streams at once (each call with a workspace of its own).
+ * `offsets` must ascend from 0 to at most the number of slots, `order` and `slots` be each other's inverse: entries that
+ * name no row or place are not followed (no memory outside the arguments is touched), the outputs that
+ * they concern are unspecified.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Largest rank of an adapter. */
+#define TERNARY_MAX_RANK 128
+
+/*
+ * ternary_sort_slots - the token slots sorted by given indices.
+ *   ids       int32 [T, top_k]: the expert (or adapter) of each slot; outside [0, E): none.  A token may name one
+ *             more than once.
+ *   T, E      0 <= T <= 2^24, 1 <= E <= TERNARY_MAX_EXPERTS, 1 <= top_k <= TERNARY_MAX_TOP_K,
+ *             T * top_k < 2^31.
+ *   ones      fp32 [T, top_k] output of 1 (weights for ternary_combine), or NULL.
+ *   offsets, order, slots  outputs as of ternary_route: order holds the slots t * top_k + j by expert, those of one
+ *             ascending, -1 from offsets[E] on; slots each slot's place, -1 if it has none.
+ *   workspace device memory of ternary_sort_slots_workspace(T, top_k, E) bytes, 16-byte
+ *             aligned (NULL where that is 0), written before it is read.
+ * All pointers 4-byte aligned; no output may overlap ids or another.
+ */
+int ternary_sort_slots(const int32_t *ids, int64_t T, int top_k, int64_t E, float *ones, int32_t *offsets,
+                       int32_t *order, int32_t *slots, void *workspace, hipStream_t stream);
+
+/* Bytes of its workspace (0 for few slots), or TERNARY_ERR_SHAPE. */
+int64_t ternary_sort_slots_workspace(int64_t T, int top_k, int64_t E);
+
+/*
+ * ternary_dispatch - each token's row at the places of its slots:
+ *     out[slots[t, j], n] = weights[t, j] * x[t, n]
+ *   x        [T, N], dtype `dtype` (TERNARY_BF16, TERNARY_FP16, TERNARY_FP32).
+ *   slots    int32 [T, top_k]; a slot outside [0, R) is left out.
+ *   weights  fp32 [T, top_k], or NULL: rows are copied.
+ *   out      [R, N] of the same dtype; must not overlap an input.  Rows that no slot names are left as they were.
+ * Pointers aligned to their elements' size.  One fp32 product, rounded once.  0 <= T, N <= 2^24, 0 <= R < 2^31,
+ * T * top_k < 2^31, T * N and R * N up to 2^38 (for the two functions below as well).
+ */
+int ternary_dispatch(const void *x, int dtype, int64_t T, int64_t N, const int32_t *slots, const float *weights,
+                     int top_k, int64_t R, void *out, hipStream_t stream);
+
+/*
+ * ternary_dispatch_backward - gradient of ternary_dispatch:
+ *     dx[t, n] = add[t, n] + sum_j weights[t, j] * grad[slots[t, j], n]
+ *     dweights[t, j] = sum_n x[t, n] * grad[slots[t, j], n]
+ *   grad     [R, N], dtype `dtype`; rows that no slot names are not read.
+ *   weights, x, dweights  those of the forward call and an fp32 [T, top_k] output, or NULL all three
+ *            (an unweighted dispatch: weights of 1).  A slot without a place has dweights 0.
+ *   add      [T, N] (another gradient of x), or NULL; may be dx itself.
+ *   dx       [T, N] output; must not overlap the other inputs.
+ * Sums in fp32: dx add first, then j ascending, rounded once; dweights in an order that depends on N alone.
+ */
+int ternary_dispatch_backward(const void *grad, int dtype, int64_t R, int64_t N, const int32_t *slots,
+                              const float *weights, int64_t T, int top_k, const void *x, const void *add, void *dx,
+                              float *dweights, hipStream_t stream);
+
+/*
+ * ternary_combine_backward - gradient of ternary_combine (that of its `add` is grad itself):
+ *     dy[slots[t, j], n] = weights[t, j] * grad[t, n]
+ *     dweights[t, j] = sum_n y[slots[t, j], n] * grad[t, n]
+ *   grad     [T, N], y and dy [R, N], dtype `dtype`; rows of y that no slot names are not read, those of dy left as
+ *            they were.  dweights fp32 [T, top_k], 0 for a slot without a place.
+ * No output may overlap an input or the other output.
+ */
+int ternary_combine_backward(const void *grad, const void *y, int dtype, int64_t R, int64_t N, const int32_t *slots,
+                             const float *weights, int64_t T, int top_k, void *dy, float *dweights, hipStream_t stream);
+
+/*
+ * ternary_linear_adapters - low-rank adapters beside a projection, each token with its own:
+ *     y[t] = add[t] + scale[e] * (x[t] a_e^T) b_e^T,  e the adapter of token t
+ *   x          [T, K], dtype `dtype` (TERNARY_BF16 or TERNARY_FP16), as are a, b, add and y.
+ *   a, b       [E, rank, K] and [E, N, rank]; an adapter of a smaller rank is filled up with zeros.
+ *   T, K, N    0 <= T <= 2^24, 1 <= K, N <= 2^24, T * K and T * N up to 2^38; T == 0 is a successful no-op.
+ *   rank, E    1 <= rank <= TERNARY_MAX_RANK, 1 <= E <= TERNARY_MAX_EXPERTS.
+ *   scale      fp32 [E], or NULL for 1.
+ *   offsets, order, slots  of ternary_sort_slots with top_k = 1.
+ *   add        [T, N] (the projection's output), or NULL for none; may be y itself.
+ *   y          [T, N] output.  A token without an adapter gets add, or 0.
+ *   hidden     fp32 [T, rank] output x[t] a_e^T for the gradient, 16-byte aligned, or NULL; rows of tokens without an
+ *              adapter are left as they were.
+ *   workspace  device memory of ternary_linear_adapters_workspace() bytes, 16-byte aligned, written before it is read.
+ * The other pointers aligned to their elements' size; no output may overlap an input (but add) or another.
+ * Products are exact and their sums fp32, in an order that depends on the sizes alone; x a^T enters the second
+ * product as two 16-bit numbers, within 2^-17 of it (bf16; fp16: 2^-22 of the row's largest); y is rounded once.
+ * What one token holds (an infinity, a NaN) reaches that token's outputs only.
+ */
+int ternary_linear_adapters(const void *x, int dtype, int64_t T, int64_t K, int64_t N, int64_t rank, const void *a,
+                            const void *b, int64_t E, const float *scale, const int32_t *offsets,
+                            const int32_t *order, const int32_t *slots, const void *add, void *y, float *hidden,
+                            void *workspace, hipStream_t stream);
+
+/* Bytes of its workspace, or TERNARY_ERR_SHAPE. */
+int64_t ternary_linear_adapters_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E);
+
+/*
+ * ternary_linear_adapters_backward - its gradients, from grad [T, N], that of y (which is add's own as well):
+ *     dv[t] = scale[e] * grad[t] b_e,   dx[t] = add[t] + dv[t] a_e
+ *     da[e] = sum dv[t]^T x[t],         db[e] = scale[e] * sum grad[t]^T hidden[t],  over the adapter's tokens
+ *   hidden    fp32 [T, rank] as the forward call wrote it, 16-byte aligned.
+ *   add       [T, K] (another gradient of x), or NULL; may be dx itself.
+ *   dx        [T, K] output.  A token without an adapter gets add, or 0.
+ *   da, db    [E, rank, K] and [E, N, rank] outputs, 16-byte aligned; 0 for an adapter without tokens (with T == 0: all).
+ *   workspace device memory of ternary_linear_adapters_backward_workspace() bytes, 16-byte aligned.
+ * dv and hidden enter their second products as two 16-bit numbers as above (fp16, in da and db: 2^-22 of the
+ * largest of some of the adapter's tokens); every output is rounded once.  The rest as above.
+ */
+int ternary_linear_adapters_backward(const void *grad, const void *x, const float *hidden, int dtype, int64_t T,
+                                     int64_t K, int64_t N, int64_t rank, const void *a, const void *b, int64_t E,
+                                     const float *scale, const int32_t *offsets, const int32_t *order,
+                                     const int32_t *slots, const void *add, void *dx, void *da, void *db,
+                                     void *workspace, hipStream_t stream);
+
+/* Bytes of its workspace, or TERNARY_ERR_SHAPE. */
+int64_t ternary_linear_adapters_backward_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E);
+
 #ifdef __cplusplus
 }
 #endif
