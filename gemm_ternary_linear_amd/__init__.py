@@ -19,6 +19,7 @@ CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 from pathlib import Path
 from typing import NamedTuple
 
@@ -650,14 +651,18 @@ def _ptr(t: torch.Tensor | None):
     return None if t is None else t.data_ptr()
 
 
-def _workspace(name: str, like: torch.Tensor, *sizes):
-    """A new workspace of the size that library function `name` gives; None where it needs none."""
-    fn = _fns.get(name)
-    if fn is None:
-        fn = _fns[name] = getattr(lib(), name)
-    need = fn(*sizes)
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name: str, *sizes) -> int:
+    """What library function `name` gives for these sizes."""
+    need = getattr(lib(), name)(*sizes)
     if need < 0:
         raise TernaryError(need, name.removesuffix("_workspace"))
+    return need
+
+
+def _workspace(name: str, like: torch.Tensor, *sizes):
+    """A new workspace of the size that library function `name` gives; None where it needs none."""
+    need = _workspace_bytes(name, *sizes)
     return like.new_empty(need, dtype=torch.uint8) if need else None
 
 

@@ -30,9 +30,11 @@ namespace ternary {
 namespace {
 
 constexpr int kWaves = 4, kThreads = kWaves * 64;
-constexpr int kUpRows = 64;    // places of an up tile
+constexpr int kDownWaves = 4, kDownThreads = kDownWaves * 64;
 constexpr int kCols = 256;     // columns of an up or outer workgroup: 64 a wave
-constexpr int kStep = 32;      // tokens of a step of outer
+constexpr int kStep = 64;      // tokens of a step of outer
+constexpr int kOuterThreads = 512;
+constexpr int kMaxPiece = 1024;  // most tokens of a piece of outer
 
 template <int DT>
 __device__ __forceinline__ f32x4_t mfma(u32x4_v a, u32x4_v b, f32x4_t c)
@@ -85,34 +87,53 @@ __device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo)
     lo = fabsf(v) == INFINITY ? (uint16_t)0 : round_out<H>(v - h);
 }
 
-// fp32 rows [T, rank] held as `parts` partial sums, `stride` elements apart.
+// fp32 rows [T, rank] held as `parts` (1, 2, 4 or 8) partial sums, `stride` elements apart.
 struct Small {
     const float *p;
     int parts, rank;
     int64_t stride;
 };
-__device__ __forceinline__ void load_small(const Small &s, int64_t t, int j0, float v[8])
+template <int PARTS>
+__device__ __forceinline__ void load_parts(const Small &s, const float *p, int left, float v[8])
 {
+    // (all loads go out together, the sums are in order)
+    if (s.rank % 4 == 0) {
+        f32x4_t u[PARTS][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        v[i] = 0.f;
-    const float *p = s.p + t * s.rank + j0;
-    for (int k = 0; k < s.parts; ++k, p += s.stride) {
-        if (s.rank % 4 == 0) {
+        for (int k = 0; k < PARTS; ++k)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (j0 + 4 * h < s.rank) {
-                    const f32x4_t u = *reinterpret_cast<const f32x4_t *>(p + 4 * h);
+                u[k][h] = 4 * h < left ? *reinterpret_cast<const f32x4_t *>(p + k * s.stride + 4 * h) : f32x4_t{};
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[4 * h + i] += u[i];
-                }
-        } else {
+        for (int k = 0; k < PARTS; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] += j0 + i < s.rank ? p[i] : 0.f;
-        }
+                v[i] = k ? v[i] + u[k][i / 4][i % 4] : u[k][i / 4][i % 4];
+    } else {
+        float u[PARTS][8];
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                u[k][i] = i < left ? p[k * s.stride + i] : 0.f;
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                v[i] = k ? v[i] + u[k][i] : u[k][i];
     }
+}
+__device__ __forceinline__ void load_small(const Small &s, int64_t t, int j0, float v[8])
+{
+    const float *p = s.p + t * s.rank + j0;
+    if (s.parts == 1)
+        load_parts<1>(s, p, s.rank - j0, v);
+    else if (s.parts == 2)
+        load_parts<2>(s, p, s.rank - j0, v);
+    else if (s.parts == 4)
+        load_parts<4>(s, p, s.rank - j0, v);
+    else
+        load_parts<8>(s, p, s.rank - j0, v);
 }
 
 // The exponent that brings the largest finite |v[i]| to 1 .. 2 (0 where all are 0).
@@ -162,60 +183,88 @@ struct DownArgs {
 };
 
 // A workgroup takes 16 MF places and a share of the row; its waves take turns at 64 elements of it (whole
-// cache lines) and meet at the end.
+// cache lines), the next turn's loads under way meanwhile, and meet at the end.  Rows are loaded as they lie, eight
+// neighbouring lanes a line, and pass through LDS into operands: loaded as operands, with neighbouring lanes
+// in different rows, each lane would cost L1 an access.
 template <int DT, int RF, int MF, bool TR, bool WIDE>
-__global__ void __launch_bounds__(kThreads) down_kernel(const DownArgs a)
+__global__ void __launch_bounds__(kDownThreads) down_kernel(const DownArgs a)
 {
-    constexpr int RP = RF * 16, LD = RP + 8;
-    constexpr int STAGE = TR ? kWaves * 64 * LD * 2 : 0, SUMS = kWaves * MF * 64 * 16;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[STAGE > SUMS ? STAGE : SUMS];
+    constexpr int RP = RF * 16, PER = RP / 8, LD = TR ? RP + 8 : 64 + 8;
+    constexpr int WG = TR ? 32 : RP < 32 ? RP : 32;  // rows of weights that pass through LDS at a time
+    constexpr int STAGE = (WG * LD > 16 * MF * 72 ? WG * LD : 16 * MF * 72) * 2, SUMS = MF * 64 * 16;
+    __shared__ __attribute__((aligned(16))) unsigned char lds[kDownWaves * (STAGE > SUMS ? STAGE : SUMS)];
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tile = blockIdx.x / a.splits, part = blockIdx.x - tile * a.splits;
     int e, r0, r1;
     if (!find_tile<16 * MF>(a.offsets, a.E, a.T, tile, e, r0, r1))
         return;
-    int tok[MF];
+    int tok[2 * MF];
 #pragma unroll
-    for (int m = 0; m < MF; ++m)
-        tok[m] = token_at(a.order, r0 + m * 16 + col, r1, a.T);
+    for (int m = 0; m < 2 * MF; ++m)
+        tok[m] = token_at(a.order, r0 + m * 8 + lane / 8, r1, a.T);
     f32x4_t acc[RF][MF] = {};
     const int steps = (a.L + 63) / 64;
     const int lo = (int)((int64_t)steps * part / a.splits), hi = (int)((int64_t)steps * (part + 1) / a.splits);
     const uint16_t *w = a.w + (int64_t)e * a.rank * a.L;
-    uint16_t *stage = reinterpret_cast<uint16_t *>(lds) + wave * 64 * LD;
-    for (int i = lo + wave; i < hi; i += kWaves) {
-        const int k0 = i * 64;
+    uint16_t *stage = reinterpret_cast<uint16_t *>(lds) + wave * (STAGE / 2);
+    u32x4_v nx[2 * MF], nw[2 * RF];
+    auto fetch = [&](int i) {
+        const int k0 = i * 64, k = k0 + lane % 8 * 8;
+#pragma unroll
+        for (int m = 0; m < 2 * MF; ++m)
+            nx[m] = tok[m] >= 0 ? row_piece<WIDE>(a.x + (int64_t)tok[m] * a.L, k, a.L) : u32x4_v{};
+#pragma unroll
+        for (int q = 0; q < 2 * RF; ++q) {
+            if constexpr (TR) {
+                const int row = (lane + q * 64) / PER, j = (lane + q * 64) % PER * 8;
+                nw[q] = k0 + row < a.L ? row_piece<WIDE>(w + (int64_t)(k0 + row) * a.rank, j, a.rank) : u32x4_v{};
+            } else {
+                const int j = q * 8 + lane / 8;
+                nw[q] = j < a.rank ? row_piece<WIDE>(w + (int64_t)j * a.L, k, a.L) : u32x4_v{};
+            }
+        }
+    };
+    auto order = []() { asm volatile("" ::: "memory"); };  // (a wave's LDS accesses are in order)
+    if (lo + wave < hi)
+        fetch(lo + wave);
+    for (int i = lo + wave; i < hi; i += kDownWaves) {
         u32x4_v xf[2][MF], wf[2][RF];
+#pragma unroll
+        for (int m = 0; m < 2 * MF; ++m)
+            *reinterpret_cast<u32x4_v *>(stage + (m * 8 + lane / 8) * 72 + lane % 8 * 8) = nx[m];
+        order();
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int m = 0; m < MF; ++m)
-                xf[h][m] = tok[m] >= 0 ? row_piece<WIDE>(a.x + (int64_t)tok[m] * a.L, k0 + h * 32 + g * 8, a.L) : u32x4_v{};
-        if constexpr (TR) {
-            constexpr int PER = RP / 8;  // pieces of a row
+                xf[h][m] = *reinterpret_cast<const u32x4_v *>(stage + (m * 16 + col) * 72 + h * 32 + g * 8);
+        order();
+        // weights: 32 of the row (TR), or 32 of the rank, at a time
 #pragma unroll
-            for (int q = 0; q < PER; ++q) {
-                const int row = (lane + q * 64) / PER, j = (lane + q * 64) % PER * 8;
-                const u32x4_v v = k0 + row < a.L ? row_piece<WIDE>(w + (int64_t)(k0 + row) * a.rank, j, a.rank) : u32x4_v{};
-                *reinterpret_cast<u32x4_v *>(stage + row * LD + j) = v;
+        for (int part = 0; part < (TR ? 2 : RP / WG); ++part) {
+            constexpr int NQ = TR ? WG * PER / 64 : WG / 8;
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                const int p = TR ? (lane + q * 64) / PER * LD + (lane + q * 64) % PER * 8 : (q * 8 + lane / 8) * LD + lane % 8 * 8;
+                *reinterpret_cast<u32x4_v *>(stage + p) = nw[part * NQ + q];
             }
-            asm volatile("" ::: "memory");  // (a wave's LDS accesses are in order)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
+            order();
+            if constexpr (TR) {
 #pragma unroll
                 for (int f = 0; f < RF; ++f)
-                    wf[h][f] = read_transposed(stage + (h * 32 + g * 8 + col / 4) * LD + f * 16 + col % 4 * 4, LD);
-            asm volatile("" ::: "memory");
-        } else {
+                    wf[part][f] = read_transposed(stage + (g * 8 + col / 4) * LD + f * 16 + col % 4 * 4, LD);
+            } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                for (int f = 0; f < WG / 16; ++f)
 #pragma unroll
-                for (int f = 0; f < RF; ++f) {
-                    const int j = f * 16 + col;
-                    wf[h][f] = j < a.rank ? row_piece<WIDE>(w + (int64_t)j * a.L, k0 + h * 32 + g * 8, a.L) : u32x4_v{};
-                }
+                    for (int h = 0; h < 2; ++h)
+                        wf[h][part * (WG / 16) + f] = *reinterpret_cast<const u32x4_v *>(stage + (f * 16 + col) * LD + h * 32 + g * 8);
+            }
+            order();
         }
+        if (i + kDownWaves < hi)
+            fetch(i + kDownWaves);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -235,10 +284,10 @@ __global__ void __launch_bounds__(kThreads) down_kernel(const DownArgs a)
         for (int m = 0; m < MF; ++m)
             sums[(wave * MF + m) * 64 + lane] = acc[f][m];
         __syncthreads();
-        for (int m = wave; m < MF; m += kWaves) {
+        for (int m = wave; m < MF; m += kDownWaves) {
             f32x4_t v = sums[m * 64 + lane];
 #pragma unroll
-            for (int u = 1; u < kWaves; ++u)
+            for (int u = 1; u < kDownWaves; ++u)
                 v += sums[(u * MF + m) * 64 + lane];
             const int t = token_at(a.order, r0 + m * 16 + col, r1, a.T), j = f * 16 + g * 4;
             if (t >= 0) {
@@ -270,26 +319,30 @@ struct UpArgs {
     int chunks, per;  // runs of 256 columns; how many a workgroup takes
 };
 
-// A wave takes 64 columns: rows of the matrix operand in an order that leaves a lane with 16 neighbouring columns of
-// a token.  Its weights stay in registers while the tile's places pass.
-template <int DT, int RF, bool TR, bool WIDE>
+// A workgroup takes 16 MF places and runs of 256 columns, 64 a wave, whose weights stay in registers while the places
+// pass.  Weights, what is added to and y go between memory and the wave as they lie, eight neighbouring lanes a line, and
+// pass through LDS into operands and out of results, a wave by itself.
+template <int DT, int RF, int MF, bool TR, bool WIDE>
 __global__ void __launch_bounds__(kThreads) up_kernel(const UpArgs a)
 {
-    constexpr int RP = RF * 16, LDV = 2 * RP + 8, LDW = kCols + 16;
+    constexpr int ROWS = MF * 16, RP = RF * 16, PER = RP / 8, LDV = 2 * RP + 8, LDO = 64 + 4;
     constexpr int QW = RP < 32 ? 1 : RP / 32, Q = 2 * RP / 32;  // operands of the weights, and of v
-    __shared__ __attribute__((aligned(16))) uint16_t sv[kUpRows * LDV];
-    __shared__ __attribute__((aligned(16))) uint16_t sw[TR ? RP * LDW : 8];
-    __shared__ float factor[kUpRows];
-    __shared__ int toks[kUpRows];
+    // weights that pass through LDS at a time: rows of [rank, C] (TR), or columns
+    constexpr int GR = TR ? (RP < 32 ? RP : 32) : (RP <= 32 ? 64 : 16), LDW = TR ? 64 + 8 : RP + 8;
+    constexpr int STAGE = 16 * LDO * 4 > GR * LDW * 2 ? 16 * LDO * 4 : GR * LDW * 2;
+    __shared__ __attribute__((aligned(16))) uint16_t sv[ROWS * LDV];
+    __shared__ __attribute__((aligned(16))) unsigned char lds[kWaves * STAGE];
+    __shared__ float factor[ROWS];
+    __shared__ int toks[ROWS];
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int runs = (a.chunks + a.per - 1) / a.per;
     const int tile = blockIdx.x / runs, run = blockIdx.x - tile * runs;
     const int c0 = run * a.per, c1 = min(a.chunks, c0 + a.per);
-    // tokens without an adapter, 64 of them looked at by each tile
-    if (a.y != a.add && (int64_t)tile * kUpRows < a.T)
-        for (int row = tid / 32; row < kUpRows; row += kThreads / 32) {
-            const int64_t t = (int64_t)tile * kUpRows + row;
+    // tokens without an adapter, as many looked at by each tile as it has rows
+    if (a.y != a.add && (int64_t)tile * ROWS < a.T)
+        for (int row = tid / 32; row < ROWS; row += kThreads / 32) {
+            const int64_t t = (int64_t)tile * ROWS + row;
             if (t >= a.T || (unsigned)a.slots[t] < (unsigned)a.T)
                 continue;
             for (int n = c0 * kCols + tid % 32 * 8; n < min(c1 * kCols, a.C); n += kCols) {
@@ -300,15 +353,14 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const UpArgs a)
             }
         }
     int e, r0, r1;
-    if (!find_tile<kUpRows>(a.offsets, a.E, a.T, tile, e, r0, r1))
+    if (!find_tile<ROWS>(a.offsets, a.E, a.T, tile, e, r0, r1))
         return;
     const float s = a.scale ? a.scale[e] : 1.f;
     // v, in 16-bit halves; RP / 8 threads a row
-    constexpr int PER = RP / 8;
 #pragma unroll
-    for (int base = 0; base < kUpRows * PER; base += kThreads) {
+    for (int base = 0; base < ROWS * PER; base += kThreads) {
         const int i = base + tid, row = i / PER, j0 = i % PER * 8;
-        if (kUpRows * PER % kThreads != 0 && row >= kUpRows)
+        if (ROWS * PER % kThreads != 0 && row >= ROWS)
             break;
         const int t = token_at(a.order, r0 + row, r1, a.T);
         float v[8] = {};
@@ -332,72 +384,90 @@ __global__ void __launch_bounds__(kThreads) up_kernel(const UpArgs a)
         if (j0 == 0)
             factor[row] = ldexpf(s, ex), toks[row] = t;
     }
+    __syncthreads();
     const uint16_t *w = a.w + (int64_t)e * a.rank * a.C;
+    uint16_t *sw = reinterpret_cast<uint16_t *>(lds + wave * STAGE);
+    float *so = reinterpret_cast<float *>(lds + wave * STAGE);
+    auto order = []() { asm volatile("" ::: "memory"); };  // (a wave's LDS accesses are in order)
     for (int c = c0; c < c1; ++c) {
-        const int n0 = c * kCols + wave * 64;  // this wave's columns
-        u32x4_v wf[4][QW];
-        if constexpr (TR) {
-            __syncthreads();
+        const int n0 = c * kCols + wave * 64, n = n0 + lane % 8 * 8;  // this wave's columns, this lane's
+        constexpr int NW = TR ? RP / 8 : PER;
+        u32x4_v raw[NW], wf[4][QW];
 #pragma unroll
-            for (int base = 0; base < RP * 32; base += kThreads) {
-                const int row = (base + tid) / 32, n = tid % 32 * 8;
-                const u32x4_v v = row < a.rank ? row_piece<WIDE>(w + (int64_t)row * a.C, c * kCols + n, a.C) : u32x4_v{};
-                *reinterpret_cast<u32x4_v *>(sw + row * LDW + n) = v;
+        for (int i = 0; i < NW; ++i)
+            if constexpr (TR) {
+                const int j = i * 8 + lane / 8;
+                raw[i] = j < a.rank ? row_piece<WIDE>(w + (int64_t)j * a.C, n, a.C) : u32x4_v{};
+            } else {
+                const int r = (i * 64 + lane) / PER, j = (i * 64 + lane) % PER * 8;
+                raw[i] = n0 + r < a.C ? row_piece<WIDE>(w + (int64_t)(n0 + r) * a.rank, j, a.rank) : u32x4_v{};
             }
-            __syncthreads();
+        Raw<DT> base[MF][2];
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
+        for (int m = 0; m < MF; ++m)
 #pragma unroll
-                for (int q = 0; q < QW; ++q) {
-                    // lane group g: rows 8 g on of 32; of a rank of 16 they are there twice (v's halves)
-                    const int j = RP < 32 ? (g & 1) * 8 : q * 32 + g * 8;
-                    wf[f][q] = read_transposed(sw + (j + col / 4) * LDW + wave * 64 + col % 4 * 16 + f * 4, LDW);
-                }
-        } else {
-#pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                const int n = n0 + col / 4 * 16 + f * 4 + col % 4;
-#pragma unroll
-                for (int q = 0; q < QW; ++q) {
-                    const int j = RP < 32 ? (g & 1) * 8 : q * 32 + g * 8;
-                    wf[f][q] = n < a.C ? row_piece<WIDE>(w + (int64_t)n * a.rank, j, a.rank) : u32x4_v{};
-                }
+            for (int h = 0; h < 2; ++h) {
+                const int t = toks[m * 16 + h * 8 + lane / 8];
+                base[m][h] = Raw<DT>{};
+                if (a.add && t >= 0)
+                    base[m][h] = load_piece<DT, WIDE, (MF > 2)>(a.add, (int64_t)t * a.C + n, a.C - n);
             }
-            if (c == c0)
-                __syncthreads();
+        // (rows of the matrix operand: f 16 + 0 .. 15)
+#pragma unroll
+        for (int p = 0; p < (TR ? RP : 64) / GR; ++p) {
+            constexpr int NP = TR ? GR / 8 : GR * PER / 64;
+            order();
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                const int at = TR ? (i * 8 + lane / 8) * LDW + lane % 8 * 8 : (i * 64 + lane) / PER * LDW + (i * 64 + lane) % PER * 8;
+                *reinterpret_cast<u32x4_v *>(sw + at) = raw[p * NP + i];
+            }
+            order();
+            // lane group g: j = 8 g on of 32; of a rank of 16 they are there twice (v's halves)
+            if constexpr (TR) {
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+                    wf[f][p] = read_transposed(sw + ((RP < 32 ? g & 1 : g) * 8 + col / 4) * LDW + f * 16 + col % 4 * 4, LDW);
+            } else {
+#pragma unroll
+                for (int f = 0; f < GR / 16; ++f)
+#pragma unroll
+                    for (int q = 0; q < QW; ++q)
+                        wf[p * (GR / 16) + f][q] =
+                            *reinterpret_cast<const u32x4_v *>(sw + (f * 16 + col) * LDW + (RP < 32 ? (g & 1) * 8 : q * 32 + g * 8));
+            }
         }
-        const int n = n0 + g * 16;
 #pragma unroll
-        for (int m = 0; m < kUpRows / 16; ++m) {
+        for (int m = 0; m < MF; ++m) {
             if (r0 + m * 16 >= r1)
                 break;
-            const int row = m * 16 + col, t = toks[row];
-            Raw<DT> base[2] = {};
-            if (a.add && t >= 0)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (n + h * 8 < a.C)
-                        base[h] = load_piece<DT, WIDE>(a.add, (int64_t)t * a.C + n + h * 8, a.C - n - h * 8);
             f32x4_t acc[4] = {};
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                const u32x4_v vf = *reinterpret_cast<const u32x4_v *>(sv + row * LDV + q * 32 + g * 8);
+                const u32x4_v vf = *reinterpret_cast<const u32x4_v *>(sv + (m * 16 + col) * LDV + q * 32 + g * 8);
 #pragma unroll
                 for (int f = 0; f < 4; ++f)
                     acc[f] = mfma<DT>(wf[f][q % QW], vf, acc[f]);
             }
-            const float by = factor[row];
-            if (t >= 0)
+            const float by = factor[m * 16 + col];
+            order();
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (n + h * 8 < a.C) {
-                        float o[8];
-                        widen_piece(base[h], o);
+            for (int f = 0; f < 4; ++f)
+                *reinterpret_cast<f32x4_t *>(so + col * LDO + f * 16 + g * 4) = acc[f] * by;
+            order();
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            o[i] += by * acc[2 * h + i / 4][i % 4];
-                        store_piece<DT, WIDE>(a.y, (int64_t)t * a.C + n + h * 8, a.C - n - h * 8, round_piece<DT>(o));
-                    }
+            for (int h = 0; h < 2; ++h) {
+                const int row = h * 8 + lane / 8, t = toks[m * 16 + row];
+                const f32x4_t lo = *reinterpret_cast<const f32x4_t *>(so + row * LDO + lane % 8 * 8);
+                const f32x4_t hi = *reinterpret_cast<const f32x4_t *>(so + row * LDO + lane % 8 * 8 + 4);
+                float o[8];
+                widen_piece(base[m][h], o);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    o[i] += i < 4 ? lo[i % 4] : hi[i % 4];
+                if (t >= 0 && n < a.C)
+                    store_piece<DT, WIDE, (MF > 2)>(a.y, (int64_t)t * a.C + n, a.C - n, round_piece<DT>(o));
+            }
         }
     }
 }
@@ -419,25 +489,31 @@ struct OuterArgs {
     int piece, partials;  // tokens of a piece; pieces that `partial` has room for
 };
 
-// A workgroup takes a piece of an adapter's tokens and 256 columns, 64 a wave.  Steps of 32 tokens pass through LDS
-// as they lie, and both operands are read transposed; the next step's loads are under way meanwhile.
+// A workgroup takes a piece of an adapter's tokens and 256 columns: 64 columns a wave, every second 32 tokens to each
+// half of the waves, whose sums meet at the end.  Steps of 64 tokens pass through LDS as they lie, and both operands are
+// read transposed; the next step's loads are under way meanwhile.
 // BY_RANK: the output is [E, rank, C], else [E, C, rank].
 template <int DT, int RF, bool WIDE, bool BY_RANK>
 __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProblem &p, int idx, int c0, uint16_t *sd,
-                                            uint16_t *sv, float *most)
+                                            uint16_t *sv, int *toks, float *most)
 {
     constexpr int RP = RF * 16, LDV = 2 * RP + 8, LDD = kCols + 16;
-    constexpr int PER = RP / 8, NV = (kStep * PER + kThreads - 1) / kThreads, ND = kStep * 32 / kThreads;
+    constexpr int PER = RP / 8, NV = (kStep * PER + kOuterThreads - 1) / kOuterThreads, ND = kStep * 32 / kOuterThreads;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = wave / 4, cols = wave % 4 * 64;
     int e, r0, r1, pieces, number;
     if (!find_piece(a.offsets, a.E, a.T, a.piece, idx, e, r0, r1, pieces, number) || (pieces > 1 && number >= a.partials))
         return;
+    const int len = (r1 - r0 + kStep - 1) / kStep * kStep;
+    for (int i = tid; i < len; i += kOuterThreads)
+        toks[i] = token_at(a.order, r0 + i, r1, a.T);
+    __syncthreads();
     int ex = 0;
     if constexpr (DT == TERNARY_FP16) {
         float m = 0.f;
-        for (int i = tid; i < (r1 - r0) * PER; i += kThreads) {
-            const int t = token_at(a.order, r0 + i / PER, r1, a.T);
+#pragma unroll 2
+        for (int i = tid; i < len * PER; i += kOuterThreads) {
+            const int t = toks[i / PER];
             float v[8];
             if (t >= 0 && i % PER * 8 < a.rank) {
                 load_small(p.v, t, i % PER * 8, v);
@@ -450,21 +526,24 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProbl
         if (lane == 0)
             most[wave] = m;
         __syncthreads();
-        ex = exponent(fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])));
+#pragma unroll
+        for (int w = 0; w < kOuterThreads / 64; ++w)
+            m = fmaxf(m, most[w]);
+        ex = exponent(m);
     }
     u32x4_v nd[ND];
     float nv[NV][8];
     auto fetch = [&](int r) {
 #pragma unroll
         for (int q = 0; q < ND; ++q) {
-            const int row = (tid + q * kThreads) / 32, n = c0 + tid % 32 * 8;
-            const int t = token_at(a.order, r + row, r1, a.T);
+            const int row = (tid + q * kOuterThreads) / 32, n = c0 + tid % 32 * 8;
+            const int t = toks[r - r0 + row];
             nd[q] = t >= 0 ? row_piece<WIDE>(p.d + (int64_t)t * p.C, n, p.C) : u32x4_v{};
         }
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            const int i = tid + q * kThreads;
-            const int t = i / PER < kStep ? token_at(a.order, r + i / PER, r1, a.T) : -1;
+            const int i = tid + q * kOuterThreads;
+            const int t = i / PER < kStep ? toks[r - r0 + i / PER] : -1;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 nv[q][k] = 0.f;
@@ -478,25 +557,26 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProbl
         __syncthreads();
 #pragma unroll
         for (int q = 0; q < ND; ++q)
-            *reinterpret_cast<u32x4_v *>(sd + (tid + q * kThreads) / 32 * LDD + tid % 32 * 8) = nd[q];
+            *reinterpret_cast<u32x4_v *>(sd + (tid + q * kOuterThreads) / 32 * LDD + tid % 32 * 8) = nd[q];
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            const int i = tid + q * kThreads;
+            const int i = tid + q * kOuterThreads;
             if (i / PER < kStep)
                 put_split<DT, RP>(sv + i / PER * LDV, i % PER * 8, nv[q], ex);
         }
         __syncthreads();
         if (r + kStep < r1)
             fetch(r + kStep);
+        const int row = half * 32 + g * 8 + col / 4;
         u32x4_v df[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            df[c] = read_transposed(sd + (g * 8 + col / 4) * LDD + wave * 64 + c * 16 + col % 4 * 4, LDD);
+            df[c] = read_transposed(sd + row * LDD + cols + c * 16 + col % 4 * 4, LDD);
 #pragma unroll
         for (int f = 0; f < RF; ++f)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const u32x4_v vf = read_transposed(sv + (g * 8 + col / 4) * LDV + h * RP + f * 16 + col % 4 * 4, LDV);
+                const u32x4_v vf = read_transposed(sv + row * LDV + h * RP + f * 16 + col % 4 * 4, LDV);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
                     acc[c][f] = BY_RANK ? mfma<DT>(df[c], vf, acc[c][f]) : mfma<DT>(vf, df[c], acc[c][f]);
@@ -504,50 +584,60 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProbl
     }
     const int64_t size = (int64_t)a.rank * p.C;
     const float by = ldexpf(p.scale ? p.scale[e] : 1.f, ex);
+    f32x4_t *other = reinterpret_cast<f32x4_t *>(sd);  // the other half's sums, 16 of the rank at a time
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+    for (int f = 0; f < RF; ++f) {
+        __syncthreads();
+        if (half == 1)
 #pragma unroll
-        for (int f = 0; f < RF; ++f) {
-            // four neighbours of the axis that lies contiguous in the output
-            const int j = f * 16 + (BY_RANK ? col : g * 4), n = c0 + wave * 64 + c * 16 + (BY_RANK ? g * 4 : col);
-            const int64_t i = BY_RANK ? (int64_t)j * p.C + n : (int64_t)n * a.rank + j;
-            const int left = BY_RANK ? (j < a.rank ? p.C - n : 0) : (n < p.C ? a.rank - j : 0);
-            const int len = BY_RANK ? p.C : a.rank;
-            if (left <= 0)
-                continue;
-            const f32x4_t v = acc[c][f] * by;
-            if (pieces > 1) {
-                float *o = p.partial + number * size + i;
-                if (len % 4 == 0)
-                    *reinterpret_cast<f32x4_t *>(o) = v;
-                else
+            for (int c = 0; c < 4; ++c)
+                other[(wave % 4 * 4 + c) * 64 + lane] = acc[c][f];
+        __syncthreads();
+        if (half == 0)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < left)
-                            o[k] = v[k];
-            } else {
-                uint16_t *o = p.out + e * size + i;
-                if (len % 4 == 0)
-                    store4<DT>(o, 0, v);
-                else
+            for (int c = 0; c < 4; ++c) {
+                // four neighbours of the axis that lies contiguous in the output
+                const int j = f * 16 + (BY_RANK ? col : g * 4), n = c0 + cols + c * 16 + (BY_RANK ? g * 4 : col);
+                const int64_t i = BY_RANK ? (int64_t)j * p.C + n : (int64_t)n * a.rank + j;
+                const int left = BY_RANK ? (j < a.rank ? p.C - n : 0) : (n < p.C ? a.rank - j : 0);
+                const int line = BY_RANK ? p.C : a.rank;
+                const f32x4_t v = (acc[c][f] + other[(wave * 4 + c) * 64 + lane]) * by;
+                if (left <= 0)
+                    continue;
+                if (pieces > 1) {
+                    float *o = p.partial + number * size + i;
+                    if (line % 4 == 0)
+                        *reinterpret_cast<f32x4_t *>(o) = v;
+                    else
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (k < left)
-                            store_elem<DT>(o, k, v[k]);
+                        for (int k = 0; k < 4; ++k)
+                            if (k < left)
+                                o[k] = v[k];
+                } else {
+                    uint16_t *o = p.out + e * size + i;
+                    if (line % 4 == 0)
+                        store4<DT>(o, 0, v);
+                    else
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k < left)
+                                store_elem<DT>(o, k, v[k]);
+                }
             }
-        }
+    }
 }
 
 template <int DT, int RF, bool WIDE>
-__global__ void __launch_bounds__(kThreads) outer_kernel(const OuterArgs a)
+__global__ void __launch_bounds__(kOuterThreads) outer_kernel(const OuterArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint16_t sd[kStep * (kCols + 16)], sv[kStep * (RF * 32 + 8)];
-    __shared__ float most[kWaves];
+    __shared__ int toks[kMaxPiece];
+    __shared__ float most[kOuterThreads / 64];
     const int chunks = a.p[0].chunks + a.p[1].chunks, idx = blockIdx.x / chunks, at = blockIdx.x - idx * chunks;
     if (at < a.p[0].chunks)
-        outer_piece<DT, RF, WIDE, false>(a, a.p[0], idx, at * kCols, sd, sv, most);
+        outer_piece<DT, RF, WIDE, false>(a, a.p[0], idx, at * kCols, sd, sv, toks, most);
     else
-        outer_piece<DT, RF, WIDE, true>(a, a.p[1], idx, (at - a.p[0].chunks) * kCols, sd, sv, most);
+        outer_piece<DT, RF, WIDE, true>(a, a.p[1], idx, (at - a.p[0].chunks) * kCols, sd, sv, toks, most);
 }
 
 // Gradients of adapters with several pieces, and zeros for those without tokens: four neighbours a thread.
@@ -595,18 +685,20 @@ inline int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m; }
 inline int64_t tiles_of(int64_t T, int64_t E, int64_t rows) { return T / rows + (E < T ? E : T); }
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// Fragments of 16 tokens of a down tile.
-inline int down_rows(int64_t T, int64_t E, int64_t rank) { return T <= 16 * E ? 1 : rank > 64 ? 2 : 4; }
+// Fragments of 16 tokens of a down tile, and over how many workgroups its rows are split.
+inline int down_rows(int64_t T, int64_t E, int64_t rank) { return T <= 16 * E ? 1 : T >= 4096 && rank > 32 && rank <= 64 ? 4 : 2; }
 inline int down_splits(int64_t T, int64_t E, int64_t L, int64_t rank)
 {
-    const int64_t tiles = up_to(T, 16 * down_rows(T, E, rank)) + (E < T ? E : T) / 2, steps = up_to(L, 256);
-    const int64_t want = up_to(512, tiles > 0 ? tiles : 1);
-    return (int)(want < steps ? want : steps);
+    const int64_t tiles = up_to(T, 16 * down_rows(T, E, rank)) + (E < T ? E : T) / 2, steps = up_to(L, 64 * kDownWaves);
+    int s = 1;
+    while (s < 8 && s * 2 <= steps && s * tiles < 384)
+        s *= 2;
+    return s;
 }
 inline int piece_tokens(int64_t T, int64_t K, int64_t N)
 {
-    const int64_t chunks = up_to(K, kCols) + up_to(N, kCols), want = T * chunks / 1024 / kStep * kStep;
-    return (int)(want < 128 ? 128 : want > 1024 ? 1024 : want);
+    const int64_t chunks = up_to(K, kCols) + up_to(N, kCols), want = T * chunks / 384 / kStep * kStep;
+    return (int)(want < 128 ? 128 : want > kMaxPiece ? kMaxPiece : want);
 }
 inline int64_t round256(int64_t n) { return (n + 255) & ~(int64_t)255; }
 inline int64_t small_bytes(int64_t T, int64_t E, int64_t L, int64_t rank)
@@ -650,9 +742,11 @@ hipError_t launch_down(const DownArgs &d, bool fp16, hipStream_t stream)
         constexpr int DT = decltype(dt)::value, RF = decltype(rf)::value;
         constexpr bool WIDE = decltype(wd)::value;
         if (mf == 1)
-            hipLaunchKernelGGL((down_kernel<DT, RF, 1, TR, WIDE>), grid, dim3(kThreads), 0, stream, d);
-        else
-            hipLaunchKernelGGL((down_kernel<DT, RF, (RF > 4 ? 2 : 4), TR, WIDE>), grid, dim3(kThreads), 0, stream, d);
+            hipLaunchKernelGGL((down_kernel<DT, RF, 1, TR, WIDE>), grid, dim3(kDownThreads), 0, stream, d);
+        else if (RF != 4 || mf == 2)
+            hipLaunchKernelGGL((down_kernel<DT, RF, 2, TR, WIDE>), grid, dim3(kDownThreads), 0, stream, d);
+        else if constexpr (RF == 4)
+            hipLaunchKernelGGL((down_kernel<DT, RF, 4, TR, WIDE>), grid, dim3(kDownThreads), 0, stream, d);
     });
     return hipGetLastError();
 }
@@ -661,14 +755,19 @@ template <bool TR>
 hipError_t launch_up(UpArgs u, bool fp16, hipStream_t stream)
 {
     u.chunks = (int)up_to(u.C, kCols);
-    const int64_t tiles = tiles_of(u.T, u.E, kUpRows);
+    const int mf = u.T <= 2048 ? 2 : 4;
+    const int64_t tiles = tiles_of(u.T, u.E, 16 * mf);
     const int64_t per = tiles * u.chunks / 2048;
-    u.per = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+    u.per = (int)(per < 1 ? 1 : per > 2 ? 2 : per);
     const bool wide = u.C % 8 == 0 && aligned16(u.w) && aligned16(u.add) && aligned16(u.y) && (TR || u.rank % 8 == 0);
     const dim3 grid((unsigned)(tiles * up_to(u.chunks, u.per)));
     with_rank(fp16, u.rank, wide, [&](auto dt, auto rf, auto wd) {
-        hipLaunchKernelGGL((up_kernel<decltype(dt)::value, decltype(rf)::value, TR, decltype(wd)::value>), grid,
-                           dim3(kThreads), 0, stream, u);
+        constexpr int DT = decltype(dt)::value, RF = decltype(rf)::value;
+        constexpr bool WIDE = decltype(wd)::value;
+        if (mf == 2)
+            hipLaunchKernelGGL((up_kernel<DT, RF, 2, TR, WIDE>), grid, dim3(kThreads), 0, stream, u);
+        else
+            hipLaunchKernelGGL((up_kernel<DT, RF, 4, TR, WIDE>), grid, dim3(kThreads), 0, stream, u);
     });
     return hipGetLastError();
 }
@@ -724,7 +823,7 @@ hipError_t launch_adapters_back(const AdapterArgs &a, hipStream_t stream)
         const dim3 grid((unsigned)(tiles_of(a.T, a.E, piece) * (o.p[0].chunks + o.p[1].chunks)));
         with_rank(a.fp16, a.rank, wide, [&](auto dt, auto rf, auto wd) {
             hipLaunchKernelGGL((outer_kernel<decltype(dt)::value, decltype(rf)::value, decltype(wd)::value>), grid,
-                               dim3(kThreads), 0, stream, o);
+                               dim3(kOuterThreads), 0, stream, o);
         });
         e = hipGetLastError();
         if (e != hipSuccess)

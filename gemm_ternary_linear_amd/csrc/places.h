@@ -73,8 +73,8 @@ __device__ __forceinline__ bool find_tile(const int32_t *offsets, int E, int R, 
     return find_tile_of<BM, 8>(offsets, E, R, idx, e, r0, r1);
 }
 
-// The idx-th piece of up to P places of one expert, as by find_tile; and the expert's number of
-// pieces, and where it has several the piece's number among the pieces of such experts.
+// The idx-th piece of up to P places of one expert, as by find_tile, the expert's pieces alike but for multiples of
+// 32; and its number of pieces, and where it has several the piece's number among the pieces of such experts.
 template <int EP>
 __device__ __forceinline__ bool find_piece_of(const int32_t *offsets, int E, int R, int P, int idx, int &e, int &r0,
                                               int &r1, int &pieces, int &number)
@@ -100,9 +100,10 @@ __device__ __forceinline__ bool find_piece_of(const int32_t *offsets, int E, int
 #pragma unroll
     for (int i = 0; i < EP; ++i) {
         if (left >= 0 && left < n[i]) {
+            const int a = max(o[i], 0), b = min(o[i + 1], R), len = ((b - a + n[i] - 1) / n[i] + 31) & ~31;
             fe = lo + i;
-            f0 = max(o[i], 0) + left * P;
-            f1 = min(min(o[i + 1], R), f0 + P);
+            f0 = min(a + left * len, b);
+            f1 = min(b, f0 + len);
             fn = n[i];
             fs = before + left;
         }

@@ -15,8 +15,9 @@ struct Raw {
 };
 
 // The piece of eight elements at element i of p, `n` of which belong to the row (none if n <= 0); the others are 0.
-// WIDE: pieces are 16-byte aligned and rows hold whole ones.
-template <int DT, bool WIDE>
+// WIDE: pieces are 16-byte aligned and rows hold whole ones.  STREAM: what is read or written once of a large array, past
+// the caches (wide pieces only).
+template <int DT, bool WIDE, bool STREAM = false>
 __device__ __forceinline__ Raw<DT> load_piece(const void *p, int64_t i, int n)
 {
     Raw<DT> r;
@@ -25,13 +26,17 @@ __device__ __forceinline__ Raw<DT> load_piece(const void *p, int64_t i, int n)
             const float *f = static_cast<const float *>(p) + i;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if constexpr (WIDE)
+                if constexpr (WIDE && STREAM)
+                    r.d[h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_v *>(f + 4 * h));
+                else if constexpr (WIDE)
                     r.d[h] = *reinterpret_cast<const u32x4_v *>(f + 4 * h);
                 else
                     r.d[h] = *reinterpret_cast<const u32x4_a4 *>(f + 4 * h);
         } else {
             const uint16_t *f = static_cast<const uint16_t *>(p) + i;
-            if constexpr (WIDE)
+            if constexpr (WIDE && STREAM)
+                r.d[0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_v *>(f));
+            else if constexpr (WIDE)
                 r.d[0] = *reinterpret_cast<const u32x4_v *>(f);
             else
                 r.d[0] = *reinterpret_cast<const u32x4_a2 *>(f);
@@ -54,7 +59,7 @@ __device__ __forceinline__ Raw<DT> load_piece(const void *p, int64_t i, int n)
     return r;
 }
 
-template <int DT, bool WIDE>
+template <int DT, bool WIDE, bool STREAM = false>
 __device__ __forceinline__ void store_piece(void *p, int64_t i, int n, const Raw<DT> &r)
 {
     if (n >= 8) {
@@ -62,13 +67,17 @@ __device__ __forceinline__ void store_piece(void *p, int64_t i, int n, const Raw
             float *f = static_cast<float *>(p) + i;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if constexpr (WIDE)
+                if constexpr (WIDE && STREAM)
+                    __builtin_nontemporal_store(r.d[h], reinterpret_cast<u32x4_v *>(f + 4 * h));
+                else if constexpr (WIDE)
                     *reinterpret_cast<u32x4_v *>(f + 4 * h) = r.d[h];
                 else
                     *reinterpret_cast<u32x4_a4 *>(f + 4 * h) = r.d[h];
         } else {
             uint16_t *f = static_cast<uint16_t *>(p) + i;
-            if constexpr (WIDE)
+            if constexpr (WIDE && STREAM)
+                __builtin_nontemporal_store(r.d[0], reinterpret_cast<u32x4_v *>(f));
+            else if constexpr (WIDE)
                 *reinterpret_cast<u32x4_v *>(f) = r.d[0];
             else
                 *reinterpret_cast<u32x4_a2 *>(f) = r.d[0];

@@ -7,7 +7,7 @@
 // order shows in a result.
 //
 // Up to kOneSlots slots one workgroup does all (one launch).  More: a workgroup counts a chunk of
-// slots into the workspace [chunks][E]; sums over the chunks before each are made by the placing
+// slots into the workspace; sums over the chunks before each are made by the placing
 // workgroups themselves where the chunks are few, else by a kernel in between.
 #include "fp8_common.h"
 #include "internal.h"
@@ -25,6 +25,8 @@ constexpr int64_t kSmallSlots = (int64_t)1 << 17;  // most slots in chunks of 10
 constexpr int kFlatChunks = 64;                  // most chunks whose counts every workgroup adds up itself
 
 inline int chunk_slots(int64_t n) { return n <= kSmallSlots ? kThreads : kThreads * kSteps; }
+// Counts lie in rows of whole 16 bytes.
+__host__ __device__ inline int count_row(int E) { return (E + 3) & ~3; }
 inline int64_t chunks_of(int64_t n) { return (n + chunk_slots(n) - 1) / chunk_slots(n); }
 
 // The lanes of the wave whose key is this lane's (keys below 2^bits; `has` false: none).
@@ -61,7 +63,7 @@ __device__ __forceinline__ void scan_counts(int *v, int n)
     __syncthreads();
 }
 
-// Counts of every chunk of slots, [chunks][E].
+// Counts of every chunk of slots, [chunks][count_row(E)].
 __global__ void __launch_bounds__(kThreads) sort_count_kernel(const SortArgs a, int chunk)
 {
     __shared__ int count[kMaxE];
@@ -75,8 +77,8 @@ __global__ void __launch_bounds__(kThreads) sort_count_kernel(const SortArgs a, 
             atomicAdd(&count[id], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kThreads)
-        a.counts[(int64_t)blockIdx.x * a.E + e] = count[e];
+    for (int e = threadIdx.x; e < count_row(a.E); e += kThreads)
+        a.counts[(int64_t)blockIdx.x * count_row(a.E) + e] = e < a.E ? count[e] : 0;
 }
 
 // The counts become sums over the chunks before; the totals go to a row after the last.  A
@@ -89,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) sort_scan_kernel(const SortArgs a, i
     int s = 0;
     if (e < a.E)
         for (int64_t c = lo; c < hi; ++c)
-            s += a.counts[c * a.E + e];
+            s += a.counts[c * count_row(a.E) + e];
     part[row][col] = s;
     __syncthreads();
     if (e < a.E) {
@@ -97,12 +99,12 @@ __global__ void __launch_bounds__(kThreads) sort_scan_kernel(const SortArgs a, i
         for (int i = 0; i < row; ++i)
             run += part[i][col];
         for (int64_t c = lo; c < hi; ++c) {
-            const int u = a.counts[c * a.E + e];
-            a.counts[c * a.E + e] = run;
+            const int u = a.counts[c * count_row(a.E) + e];
+            a.counts[c * count_row(a.E) + e] = run;
             run += u;
         }
         if (row == 63)
-            a.counts[chunks * a.E + e] = run;
+            a.counts[chunks * count_row(a.E) + e] = run;
     }
 }
 
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(const SortArgs a, 
 {
     __shared__ int count[kWaves][kMaxE];
     __shared__ int first[kMaxE + 1], before[kMaxE];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.E;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, E = a.E, ld = count_row(E);
     const int64_t s0 = (int64_t)blockIdx.x * (kThreads * STEPS) + wave * (64 * STEPS) + lane;
     int id[STEPS], rank[STEPS];
 #pragma unroll
@@ -129,18 +131,32 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(const SortArgs a, 
         count[i / E][i % E] = 0;
     if constexpr (HOW != How::ONE)
         for (int e = tid; e < E; e += kThreads) {
-            first[e] = HOW == How::SUMMED ? a.counts[chunks * E + e] : 0;
-            before[e] = HOW == How::SUMMED ? a.counts[(int64_t)blockIdx.x * E + e] : 0;
+            first[e] = HOW == How::SUMMED ? a.counts[chunks * ld + e] : 0;
+            before[e] = HOW == How::SUMMED ? a.counts[(int64_t)blockIdx.x * ld + e] : 0;
         }
     __syncthreads();
     if constexpr (HOW == How::FLAT) {
-        for (int i = tid; i < (int)chunks * E; i += kThreads) {
-            const int v = a.counts[i], c = i / E, e = i - c * E;
-            if (v) {
-                atomicAdd(&first[e], v);
-                if (c < (int)blockIdx.x)
-                    atomicAdd(&before[e], v);
+        // four keys a thread, as many rows of counts at a time as there are threads
+        const int width = ld / 4, rows = kThreads / width, row = tid / width, e4 = tid % width * 4;
+        if (row < rows) {
+            int all[4] = {}, low[4] = {};
+#pragma unroll 4
+            for (int c = row; c < (int)chunks; c += rows) {
+                const int4 v = *reinterpret_cast<const int4 *>(a.counts + c * ld + e4);
+                const int n[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    all[i] += n[i];
+                    low[i] += c < (int)blockIdx.x ? n[i] : 0;
+                }
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (all[i]) {
+                    atomicAdd(&first[e4 + i], all[i]);
+                    if (low[i])
+                        atomicAdd(&before[e4 + i], low[i]);
+                }
         }
     }
 #pragma unroll
@@ -192,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) sort_place_kernel(const SortArgs a, 
 
 int64_t sort_slots_workspace(int64_t n, int64_t E)
 {
-    return n <= kOneSlots ? 0 : (chunks_of(n) + 1) * E * 4;
+    return n <= kOneSlots ? 0 : (chunks_of(n) + 1) * count_row((int)E) * 4;
 }
 
 hipError_t launch_sort_slots(const SortArgs &a, hipStream_t stream)
