@@ -12,7 +12,7 @@
 //     outer sums over an adapter's tokens: da and db.  Split into pieces of tokens; partial sums in fp32,
 //           added up in order by a fourth kernel where an adapter has several.
 // All products are on the matrix unit in 16 bits, their sums in fp32.  v and dv, which are fp32, enter it as
-// two 16-bit numbers, the nearest and the nearest to what that left: 2^-17 off (bf16; fp16 2^-22), far below the
+// two 16-bit numbers, cut and the nearest to what that left: 2^-16 off (bf16; fp16 2^-22), far below the
 // outputs' own rounding, for twice the matrix cycles, of which there are plenty: the
 // layer is bound by reading x and reading and writing y.  fp16 would lose what is small or large, so there
 // v is first brought to below 2 by a power of two: a row's largest (up) or the piece's (outer).
@@ -30,10 +30,13 @@ namespace ternary {
 namespace {
 
 constexpr int kWaves = 4, kThreads = kWaves * 64;
-constexpr int kDownWaves = 4, kDownThreads = kDownWaves * 64;
-constexpr int kCols = 256;     // columns of an up or outer workgroup: 64 a wave
+constexpr int kCols = 256;     // columns of an up workgroup at a time: 64 a wave
 constexpr int kStep = 64;      // tokens of a step of outer
-constexpr int kOuterThreads = 512;
+// An outer workgroup's threads, the fragments of 16 columns of a wave, and its columns (half of the waves each).
+__host__ __device__ constexpr int outer_threads(int rf) { return rf > 4 ? 1024 : 512; }
+__host__ __device__ constexpr int outer_frags(int rf) { return rf > 2 ? 2 : 4; }
+__host__ __device__ constexpr int outer_cols(int rf) { return outer_threads(rf) / 128 * 16 * outer_frags(rf); }
+inline int rank_frags(int64_t rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 constexpr int kMaxPiece = 1024;  // most tokens of a piece of outer
 
 template <int DT>
@@ -69,22 +72,22 @@ __device__ __forceinline__ u32x4_v row_piece(const uint16_t *p, int i, int n)
     return load_piece<TERNARY_BF16, WIDE>(p, i, n - i).d[0];
 }
 
-// v as two 16-bit numbers (bits): the nearest, and the nearest to the rest.
+// Two values as two 16-bit numbers each: cut, and the nearest to what that left.  (Of an infinity nothing is left, which the
+// difference gives as NaN; the maximum makes that a finite number, which changes no sum with the infinity.)
 template <int DT>
-__device__ __forceinline__ void split(float v, uint16_t &hi, uint16_t &lo)
+__device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo)
 {
-    constexpr bool H = DT == TERNARY_FP16;
-    float h;
-    if constexpr (H) {
-        hi = f32_to_f16_rne(v);
-        h = f16_bits_to_f32(hi);
+    if constexpr (DT == TERNARY_FP16) {  // |a|, |b| < 2 or not finite
+        hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+        const float x = fmaxf(a - f16_bits_to_f32((uint16_t)hi), -1.f), y = fmaxf(b - f16_bits_to_f32((uint16_t)(hi >> 16)), -1.f);
+        lo = (uint32_t)f32_to_f16_rne(x) | (uint32_t)f32_to_f16_rne(y) << 16;
     } else {
-        hi = f32_to_bf16_rne(v);
-        if ((hi & 0x7fff) == 0x7f80 && fabsf(v) < INFINITY)
-            hi -= 1;  // (the largest, where rounding went past it)
-        h = __builtin_bit_cast(float, (uint32_t)hi << 16);
+        const uint32_t u = __builtin_bit_cast(uint32_t, a), v = __builtin_bit_cast(uint32_t, b);
+        const uint32_t m = u & 0xffff0000u, n = v & 0xffff0000u;
+        hi = __builtin_amdgcn_perm(v, u, 0x07060302u);
+        const float x = fmaxf(a - __builtin_bit_cast(float, m), -0x1p121f), y = fmaxf(b - __builtin_bit_cast(float, n), -0x1p121f);
+        lo = (uint32_t)f32_to_bf16_rne(x) | (uint32_t)f32_to_bf16_rne(y) << 16;
     }
-    lo = fabsf(v) == INFINITY ? (uint16_t)0 : round_out<H>(v - h);
 }
 
 // fp32 rows [T, rank] held as `parts` (1, 2, 4 or 8) partial sums, `stride` elements apart.
@@ -132,17 +135,29 @@ __device__ __forceinline__ void load_small(const Small &s, int64_t t, int j0, fl
         load_parts<2>(s, p, s.rank - j0, v);
     else if (s.parts == 4)
         load_parts<4>(s, p, s.rank - j0, v);
-    else
-        load_parts<8>(s, p, s.rank - j0, v);
+    else {
+        float more[8];  // (in two batches, for fewer registers)
+        load_parts<4>(s, p, s.rank - j0, v);
+        load_parts<4>(s, p + 4 * s.stride, s.rank - j0, more);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] += more[i];
+    }
 }
 
-// The exponent that brings the largest finite |v[i]| to 1 .. 2 (0 where all are 0).
+// The largest finite |v[i]|, and the exponent that brings it to 1 .. 2 (0 where all are 0).
 __device__ __forceinline__ float largest(const float v[8])
 {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        m = fmaxf(m, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.f);
+        m = fmaxf(m, fabsf(v[i]));
+    if (m == INFINITY) {
+        m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            m = fmaxf(m, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.f);
+    }
     return m;
 }
 __device__ __forceinline__ int exponent(float m) { return m > 0.f ? ilogbf(m) : 0; }
@@ -151,15 +166,15 @@ __device__ __forceinline__ int exponent(float m) { return m > 0.f ? ilogbf(m) : 
 template <int DT, int RP>
 __device__ __forceinline__ void put_split(uint16_t *row, int j0, const float v[8], int ex)
 {
-    uint16_t hi[8], lo[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        split<DT>(DT == TERNARY_FP16 ? ldexpf(v[i], -ex) : v[i], hi[i], lo[i]);
     u32x4_v h, l;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        h[i] = (uint32_t)hi[2 * i] | (uint32_t)hi[2 * i + 1] << 16;
-        l[i] = (uint32_t)lo[2 * i] | (uint32_t)lo[2 * i + 1] << 16;
+        uint32_t hi, lo;
+        if constexpr (DT == TERNARY_FP16)
+            split<DT>(ldexpf(v[2 * i], -ex), ldexpf(v[2 * i + 1], -ex), hi, lo);
+        else
+            split<DT>(v[2 * i], v[2 * i + 1], hi, lo);
+        h[i] = hi, l[i] = lo;
     }
     *reinterpret_cast<u32x4_v *>(row + j0) = h;
     *reinterpret_cast<u32x4_v *>(row + RP + j0) = l;
@@ -186,13 +201,13 @@ struct DownArgs {
 // cache lines), the next turn's loads under way meanwhile, and meet at the end.  Rows are loaded as they lie, eight
 // neighbouring lanes a line, and pass through LDS into operands: loaded as operands, with neighbouring lanes
 // in different rows, each lane would cost L1 an access.
-template <int DT, int RF, int MF, bool TR, bool WIDE>
-__global__ void __launch_bounds__(kDownThreads) down_kernel(const DownArgs a)
+template <int DT, int RF, int MF, int WAVES, bool TR, bool WIDE>
+__global__ void __launch_bounds__(WAVES * 64) down_kernel(const DownArgs a)
 {
     constexpr int RP = RF * 16, PER = RP / 8, LD = TR ? RP + 8 : 64 + 8;
     constexpr int WG = TR ? 32 : RP < 32 ? RP : 32;  // rows of weights that pass through LDS at a time
     constexpr int STAGE = (WG * LD > 16 * MF * 72 ? WG * LD : 16 * MF * 72) * 2, SUMS = MF * 64 * 16;
-    __shared__ __attribute__((aligned(16))) unsigned char lds[kDownWaves * (STAGE > SUMS ? STAGE : SUMS)];
+    __shared__ __attribute__((aligned(16))) unsigned char lds[WAVES * (STAGE > SUMS ? STAGE : SUMS)];
     const int lane = threadIdx.x & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tile = blockIdx.x / a.splits, part = blockIdx.x - tile * a.splits;
@@ -228,7 +243,7 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const DownArgs a)
     auto order = []() { asm volatile("" ::: "memory"); };  // (a wave's LDS accesses are in order)
     if (lo + wave < hi)
         fetch(lo + wave);
-    for (int i = lo + wave; i < hi; i += kDownWaves) {
+    for (int i = lo + wave; i < hi; i += WAVES) {
         u32x4_v xf[2][MF], wf[2][RF];
 #pragma unroll
         for (int m = 0; m < 2 * MF; ++m)
@@ -263,8 +278,8 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const DownArgs a)
             }
             order();
         }
-        if (i + kDownWaves < hi)
-            fetch(i + kDownWaves);
+        if (i + WAVES < hi)
+            fetch(i + WAVES);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -284,10 +299,10 @@ __global__ void __launch_bounds__(kDownThreads) down_kernel(const DownArgs a)
         for (int m = 0; m < MF; ++m)
             sums[(wave * MF + m) * 64 + lane] = acc[f][m];
         __syncthreads();
-        for (int m = wave; m < MF; m += kDownWaves) {
+        for (int m = wave; m < MF; m += WAVES) {
             f32x4_t v = sums[m * 64 + lane];
 #pragma unroll
-            for (int u = 1; u < kDownWaves; ++u)
+            for (int u = 1; u < WAVES; ++u)
                 v += sums[(u * MF + m) * 64 + lane];
             const int t = token_at(a.order, r0 + m * 16 + col, r1, a.T), j = f * 16 + g * 4;
             if (t >= 0) {
@@ -489,60 +504,38 @@ struct OuterArgs {
     int piece, partials;  // tokens of a piece; pieces that `partial` has room for
 };
 
-// A workgroup takes a piece of an adapter's tokens and 256 columns: 64 columns a wave, every second 32 tokens to each
-// half of the waves, whose sums meet at the end.  Steps of 64 tokens pass through LDS as they lie, and both operands are
+// A workgroup takes a piece of an adapter's tokens and 256 columns (128 of ranks 33 to 64): 64 a wave (32 of ranks above
+// 32), every second 32 tokens to each half of the waves, whose sums meet at the end.  Steps of 64 tokens pass through LDS as they lie, and both operands are
 // read transposed; the next step's loads are under way meanwhile.
 // BY_RANK: the output is [E, rank, C], else [E, C, rank].
 template <int DT, int RF, bool WIDE, bool BY_RANK>
 __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProblem &p, int idx, int c0, uint16_t *sd,
                                             uint16_t *sv, int *toks, float *most)
 {
-    constexpr int RP = RF * 16, LDV = 2 * RP + 8, LDD = kCols + 16;
-    constexpr int PER = RP / 8, NV = (kStep * PER + kOuterThreads - 1) / kOuterThreads, ND = kStep * 32 / kOuterThreads;
+    constexpr int RP = RF * 16, LDV = 2 * RP + 8, CF = outer_frags(RF), THREADS = outer_threads(RF), HALF = THREADS / 128, COLS = outer_cols(RF), CP = COLS / 8, LDD = COLS + 16;
+    constexpr int PER = RP / 8, NV = (kStep * PER + THREADS - 1) / THREADS, ND = kStep * CP / THREADS;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = wave / 4, cols = wave % 4 * 64;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), half = wave / HALF, cols = wave % HALF * (16 * CF);
     int e, r0, r1, pieces, number;
     if (!find_piece(a.offsets, a.E, a.T, a.piece, idx, e, r0, r1, pieces, number) || (pieces > 1 && number >= a.partials))
         return;
     const int len = (r1 - r0 + kStep - 1) / kStep * kStep;
-    for (int i = tid; i < len; i += kOuterThreads)
+    for (int i = tid; i < len; i += THREADS)
         toks[i] = token_at(a.order, r0 + i, r1, a.T);
     __syncthreads();
-    int ex = 0;
-    if constexpr (DT == TERNARY_FP16) {
-        float m = 0.f;
-#pragma unroll 2
-        for (int i = tid; i < len * PER; i += kOuterThreads) {
-            const int t = toks[i / PER];
-            float v[8];
-            if (t >= 0 && i % PER * 8 < a.rank) {
-                load_small(p.v, t, i % PER * 8, v);
-                m = fmaxf(m, largest(v));
-            }
-        }
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1)
-            m = fmaxf(m, __shfl_xor(m, o));
-        if (lane == 0)
-            most[wave] = m;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kOuterThreads / 64; ++w)
-            m = fmaxf(m, most[w]);
-        ex = exponent(m);
-    }
+    int ex = -200;  // fp16: the exponent that v is brought down by, that of its largest so far
     u32x4_v nd[ND];
     float nv[NV][8];
     auto fetch = [&](int r) {
 #pragma unroll
         for (int q = 0; q < ND; ++q) {
-            const int row = (tid + q * kOuterThreads) / 32, n = c0 + tid % 32 * 8;
+            const int row = (tid + q * THREADS) / CP, n = c0 + tid % CP * 8;
             const int t = toks[r - r0 + row];
             nd[q] = t >= 0 ? row_piece<WIDE>(p.d + (int64_t)t * p.C, n, p.C) : u32x4_v{};
         }
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            const int i = tid + q * kOuterThreads;
+            const int i = tid + q * THREADS;
             const int t = i / PER < kStep ? toks[r - r0 + i / PER] : -1;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -551,16 +544,43 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProbl
                 load_small(p.v, t, i % PER * 8, nv[q]);
         }
     };
-    f32x4_t acc[4][RF] = {};
+    f32x4_t acc[CF][RF] = {};
     fetch(r0);
     for (int r = r0; r < r1; r += kStep) {
+        if constexpr (DT == TERNARY_FP16) {
+            float m = 0.f;
+#pragma unroll
+            for (int q = 0; q < NV; ++q)
+                m = fmaxf(m, largest(nv[q]));
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1)
+                m = fmaxf(m, __shfl_xor(m, o));
+            if (lane == 0)
+                most[wave] = m;
+        }
         __syncthreads();
+        if constexpr (DT == TERNARY_FP16) {
+            float m = most[0];
+#pragma unroll
+            for (int w = 1; w < THREADS / 64; ++w)
+                m = fmaxf(m, most[w]);
+            const int now = m > 0.f ? max(ex, ilogbf(m)) : ex;
+            if (now > ex) {
+                const float down = ldexpf(1.f, ex - now);
+#pragma unroll
+                for (int c = 0; c < CF; ++c)
+#pragma unroll
+                    for (int f = 0; f < RF; ++f)
+                        acc[c][f] *= down;
+                ex = now;
+            }
+        }
 #pragma unroll
         for (int q = 0; q < ND; ++q)
-            *reinterpret_cast<u32x4_v *>(sd + (tid + q * kOuterThreads) / 32 * LDD + tid % 32 * 8) = nd[q];
+            *reinterpret_cast<u32x4_v *>(sd + (tid + q * THREADS) / CP * LDD + tid % CP * 8) = nd[q];
 #pragma unroll
         for (int q = 0; q < NV; ++q) {
-            const int i = tid + q * kOuterThreads;
+            const int i = tid + q * THREADS;
             if (i / PER < kStep)
                 put_split<DT, RP>(sv + i / PER * LDV, i % PER * 8, nv[q], ex);
         }
@@ -568,9 +588,9 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProbl
         if (r + kStep < r1)
             fetch(r + kStep);
         const int row = half * 32 + g * 8 + col / 4;
-        u32x4_v df[4];
+        u32x4_v df[CF];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < CF; ++c)
             df[c] = read_transposed(sd + row * LDD + cols + c * 16 + col % 4 * 4, LDD);
 #pragma unroll
         for (int f = 0; f < RF; ++f)
@@ -578,30 +598,30 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProbl
             for (int h = 0; h < 2; ++h) {
                 const u32x4_v vf = read_transposed(sv + row * LDV + h * RP + f * 16 + col % 4 * 4, LDV);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                for (int c = 0; c < CF; ++c)
                     acc[c][f] = BY_RANK ? mfma<DT>(df[c], vf, acc[c][f]) : mfma<DT>(vf, df[c], acc[c][f]);
             }
     }
     const int64_t size = (int64_t)a.rank * p.C;
-    const float by = ldexpf(p.scale ? p.scale[e] : 1.f, ex);
+    const float by = ldexpf(p.scale ? p.scale[e] : 1.f, DT == TERNARY_FP16 ? ex : 0);
     f32x4_t *other = reinterpret_cast<f32x4_t *>(sd);  // the other half's sums, 16 of the rank at a time
 #pragma unroll
     for (int f = 0; f < RF; ++f) {
         __syncthreads();
         if (half == 1)
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                other[(wave % 4 * 4 + c) * 64 + lane] = acc[c][f];
+            for (int c = 0; c < CF; ++c)
+                other[(wave % HALF * CF + c) * 64 + lane] = acc[c][f];
         __syncthreads();
         if (half == 0)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < CF; ++c) {
                 // four neighbours of the axis that lies contiguous in the output
                 const int j = f * 16 + (BY_RANK ? col : g * 4), n = c0 + cols + c * 16 + (BY_RANK ? g * 4 : col);
                 const int64_t i = BY_RANK ? (int64_t)j * p.C + n : (int64_t)n * a.rank + j;
                 const int left = BY_RANK ? (j < a.rank ? p.C - n : 0) : (n < p.C ? a.rank - j : 0);
                 const int line = BY_RANK ? p.C : a.rank;
-                const f32x4_t v = (acc[c][f] + other[(wave * 4 + c) * 64 + lane]) * by;
+                const f32x4_t v = (acc[c][f] + other[(wave * CF + c) * 64 + lane]) * by;
                 if (left <= 0)
                     continue;
                 if (pieces > 1) {
@@ -628,16 +648,16 @@ __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProbl
 }
 
 template <int DT, int RF, bool WIDE>
-__global__ void __launch_bounds__(kOuterThreads) outer_kernel(const OuterArgs a)
+__global__ void __launch_bounds__(outer_threads(RF), 4) outer_kernel(const OuterArgs a)
 {
-    __shared__ __attribute__((aligned(16))) uint16_t sd[kStep * (kCols + 16)], sv[kStep * (RF * 32 + 8)];
+    __shared__ __attribute__((aligned(16))) uint16_t sd[kStep * (outer_cols(RF) + 16)], sv[kStep * (RF * 32 + 8)];
     __shared__ int toks[kMaxPiece];
-    __shared__ float most[kOuterThreads / 64];
+    __shared__ float most[outer_threads(RF) / 64];
     const int chunks = a.p[0].chunks + a.p[1].chunks, idx = blockIdx.x / chunks, at = blockIdx.x - idx * chunks;
     if (at < a.p[0].chunks)
-        outer_piece<DT, RF, WIDE, false>(a, a.p[0], idx, at * kCols, sd, sv, toks, most);
+        outer_piece<DT, RF, WIDE, false>(a, a.p[0], idx, at * outer_cols(RF), sd, sv, toks, most);
     else
-        outer_piece<DT, RF, WIDE, true>(a, a.p[1], idx, (at - a.p[0].chunks) * kCols, sd, sv, toks, most);
+        outer_piece<DT, RF, WIDE, true>(a, a.p[1], idx, (at - a.p[0].chunks) * outer_cols(RF), sd, sv, toks, most);
 }
 
 // Gradients of adapters with several pieces, and zeros for those without tokens: four neighbours a thread.
@@ -685,19 +705,24 @@ inline int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m; }
 inline int64_t tiles_of(int64_t T, int64_t E, int64_t rows) { return T / rows + (E < T ? E : T); }
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// Fragments of 16 tokens of a down tile, and over how many workgroups its rows are split.
+// Fragments of 16 tokens of a down tile.  A workgroup has four waves; where tiles are few 16, so that there are few partial
+// sums (not of ranks above 32, which want the registers).
 inline int down_rows(int64_t T, int64_t E, int64_t rank) { return T <= 16 * E ? 1 : T >= 4096 && rank > 32 && rank <= 64 ? 4 : 2; }
+inline int64_t down_tiles(int64_t T, int64_t E, int64_t rank) { return up_to(T, 16 * down_rows(T, E, rank)) + (E < T ? E : T) / 2; }
+inline bool down_few(int64_t T, int64_t E, int64_t rank) { return rank <= 32 && down_tiles(T, E, rank) < 192; }
+// Workgroups that share a row: until there are enough waves, or a wave has a single step.
 inline int down_splits(int64_t T, int64_t E, int64_t L, int64_t rank)
 {
-    const int64_t tiles = up_to(T, 16 * down_rows(T, E, rank)) + (E < T ? E : T) / 2, steps = up_to(L, 64 * kDownWaves);
+    const int64_t tiles = down_tiles(T, E, rank), waves = down_few(T, E, rank) ? 16 : 4, steps = up_to(L, 64 * waves);
     int s = 1;
-    while (s < 8 && s * 2 <= steps && s * tiles < 384)
+    while (s < 8 && s * 2 <= steps && s * tiles * waves < 1536)
         s *= 2;
     return s;
 }
-inline int piece_tokens(int64_t T, int64_t K, int64_t N)
+inline int piece_tokens(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
-    const int64_t chunks = up_to(K, kCols) + up_to(N, kCols), want = T * chunks / 384 / kStep * kStep;
+    const int cols = outer_cols(rank_frags(rank));
+    const int64_t chunks = up_to(K, cols) + up_to(N, cols), want = T * chunks / 256 / kStep * kStep;
     return (int)(want < 128 ? 128 : want > kMaxPiece ? kMaxPiece : want);
 }
 inline int64_t round256(int64_t n) { return (n + 255) & ~(int64_t)255; }
@@ -736,17 +761,24 @@ template <bool TR>
 hipError_t launch_down(const DownArgs &d, bool fp16, hipStream_t stream)
 {
     const int mf = down_rows(d.T, d.E, d.rank);
+    const bool few = down_few(d.T, d.E, d.rank);
     const bool wide = d.L % 8 == 0 && aligned16(d.x) && aligned16(d.w) && (!TR || d.rank % 8 == 0);
     const dim3 grid((unsigned)(tiles_of(d.T, d.E, 16 * mf) * d.splits));
     with_rank(fp16, d.rank, wide, [&](auto dt, auto rf, auto wd) {
         constexpr int DT = decltype(dt)::value, RF = decltype(rf)::value;
         constexpr bool WIDE = decltype(wd)::value;
-        if (mf == 1)
-            hipLaunchKernelGGL((down_kernel<DT, RF, 1, TR, WIDE>), grid, dim3(kDownThreads), 0, stream, d);
-        else if (RF != 4 || mf == 2)
-            hipLaunchKernelGGL((down_kernel<DT, RF, 2, TR, WIDE>), grid, dim3(kDownThreads), 0, stream, d);
-        else if constexpr (RF == 4)
-            hipLaunchKernelGGL((down_kernel<DT, RF, 4, TR, WIDE>), grid, dim3(kDownThreads), 0, stream, d);
+        auto run = [&](auto kernel, int waves) {
+            hipLaunchKernelGGL(kernel, grid, dim3(waves * 64), 0, stream, d);
+        };
+        if constexpr (RF <= 2) {
+            if (few)
+                return mf == 1 ? run(down_kernel<DT, RF, 1, 16, TR, WIDE>, 16) : run(down_kernel<DT, RF, 2, 16, TR, WIDE>, 16);
+        }
+        if constexpr (RF == 4) {
+            if (mf == 4)
+                return run(down_kernel<DT, RF, 4, 4, TR, WIDE>, 4);
+        }
+        mf == 1 ? run(down_kernel<DT, RF, 1, 4, TR, WIDE>, 4) : run(down_kernel<DT, RF, 2, 4, TR, WIDE>, 4);
     });
     return hipGetLastError();
 }
@@ -782,7 +814,7 @@ int64_t adapters_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_
 
 int64_t adapters_back_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E)
 {
-    const int64_t partials = 2 * T / piece_tokens(T, K, N);
+    const int64_t partials = 2 * T / piece_tokens(T, K, N, rank);
     return small_bytes(T, E, N, rank) + round256(partials * rank * N * 4) + round256(partials * rank * K * 4);
 }
 
@@ -801,8 +833,8 @@ hipError_t launch_adapters(const AdapterArgs &a, hipStream_t stream)
 
 hipError_t launch_adapters_back(const AdapterArgs &a, hipStream_t stream)
 {
-    const int piece = piece_tokens(a.T, a.K, a.N), splits = down_splits(a.T, a.E, a.N, a.rank);
-    const int partials = (int)(2 * (int64_t)a.T / piece);
+    const int piece = piece_tokens(a.T, a.K, a.N, a.rank), splits = down_splits(a.T, a.E, a.N, a.rank);
+    const int partials = (int)(2 * (int64_t)a.T / piece), cols = outer_cols(rank_frags(a.rank));
     char *ws = static_cast<char *>(a.workspace);
     float *dv = reinterpret_cast<float *>(ws);
     ws += small_bytes(a.T, a.E, a.N, a.rank);
@@ -811,8 +843,8 @@ hipError_t launch_adapters_back(const AdapterArgs &a, hipStream_t stream)
     float *part_a = reinterpret_cast<float *>(ws);
     const Small small = {dv, splits, a.rank, (int64_t)a.T * a.rank};
     hipError_t e = hipSuccess;
-    const OuterArgs o = {{{a.grad, {a.hidden, 1, a.rank, 0}, a.db, part_b, a.scale, a.N, (int)up_to(a.N, kCols)},
-                          {a.x, small, a.da, part_a, nullptr, a.K, (int)up_to(a.K, kCols)}},
+    const OuterArgs o = {{{a.grad, {a.hidden, 1, a.rank, 0}, a.db, part_b, a.scale, a.N, (int)up_to(a.N, cols)},
+                          {a.x, small, a.da, part_a, nullptr, a.K, (int)up_to(a.K, cols)}},
                          a.offsets, a.order, a.T, a.rank, a.E, piece, partials};
     if (a.T) {
         const DownArgs d = {a.grad, a.b, a.scale, a.offsets, a.order, dv, a.T, a.N, a.rank, a.E, splits};
@@ -823,7 +855,7 @@ hipError_t launch_adapters_back(const AdapterArgs &a, hipStream_t stream)
         const dim3 grid((unsigned)(tiles_of(a.T, a.E, piece) * (o.p[0].chunks + o.p[1].chunks)));
         with_rank(a.fp16, a.rank, wide, [&](auto dt, auto rf, auto wd) {
             hipLaunchKernelGGL((outer_kernel<decltype(dt)::value, decltype(rf)::value, decltype(wd)::value>), grid,
-                               dim3(kOuterThreads), 0, stream, o);
+                               dim3(outer_threads(decltype(rf)::value)), 0, stream, o);
         });
         e = hipGetLastError();
         if (e != hipSuccess)

@@ -617,7 +617,7 @@ int ternary_combine_backward(const void *grad, const void *y, int dtype, int64_t
  *   workspace  device memory of ternary_linear_adapters_workspace() bytes, 16-byte aligned, written before it is read.
  * The other pointers aligned to their elements' size; no output may overlap an input (but add) or another.
  * Products are exact and their sums fp32, in an order that depends on the sizes alone; x a^T enters the second
- * product as two 16-bit numbers, within 2^-17 of it (bf16; fp16: 2^-22 of the row's largest); y is rounded once.
+ * product as two 16-bit numbers, within 2^-16 of it (bf16; fp16: 2^-22 of the row's largest); y is rounded once.
  * What one token holds (an infinity, a NaN) reaches that token's outputs only.
  */
 int ternary_linear_adapters(const void *x, int dtype, int64_t T, int64_t K, int64_t N, int64_t rank, const void *a,
