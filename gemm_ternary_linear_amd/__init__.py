@@ -755,19 +755,20 @@ def combine_backward(grad: torch.Tensor, y: torch.Tensor, routing: Routing, out:
 
 def _check_adapters(x, a, b, routing, scale):
     """Shapes of adapters' operands checked against each other -> dtype code, T, K, N, rank, E."""
-    dt = _ACT.get(x.dtype)
-    if dt is None or x.dim() != 2:
+    dtype, xs, ash, bsh = x.dtype, x.shape, a.shape, b.shape
+    dt = _ACT.get(dtype)
+    if dt is None or len(xs) != 2:
         raise ValueError("x must be a 2-D bfloat16 or float16 tensor")
-    T, K = x.shape
-    if a.dim() != 3 or b.dim() != 3 or a.dtype != x.dtype or b.dtype != x.dtype or a.shape[2] != K \
-            or b.shape[0] != a.shape[0] or b.shape[2] != a.shape[1]:
+    T, K = xs
+    if len(ash) != 3 or len(bsh) != 3 or a.dtype is not dtype or b.dtype is not dtype or ash[2] != K \
+            or bsh[0] != ash[0] or bsh[2] != ash[1]:
         raise ValueError(f"a [E, rank, {K}] and b [E, N, rank] must have x's dtype and share E and rank")
-    E, rank = a.shape[:2]
+    E, rank, _ = ash
     if scale is not None and (scale.dtype != torch.float32 or scale.shape != (E,)):
         raise ValueError(f"scale must be a float32 tensor [{E}]")
     if _check_routing(routing) != (T, 1) or routing.offsets.shape != (E + 1,):
         raise ValueError(f"routing must be sort_slots() of {T} tokens' adapters, with {E + 1} offsets")
-    return dt, T, K, b.shape[1], rank, E
+    return dt, T, K, bsh[1], rank, E
 
 
 def linear_adapters(x: torch.Tensor, a: torch.Tensor, b: torch.Tensor, routing: Routing,

@@ -698,6 +698,202 @@ __global__ void __launch_bounds__(kThreads) outer_sum_kernel(const OuterArgs a, 
     }
 }
 
+// ---------------------------------------------------------------- few tokens
+
+// Few tokens of small rank: down and up in one launch.  A workgroup of 16 waves takes 16 places: its waves share the rows of x,
+// meet, and take 64 columns of y each.  Workgroups that share the places each compute v for themselves (from
+// L2), which costs less than a second launch; b and what is added to are under way meanwhile.
+struct FewArgs {
+    AdapterArgs p;
+    int chunks, per;  // runs of 1024 columns; how many a workgroup takes
+};
+constexpr int kFewWaves = 16, kFewCols = kFewWaves * 64;
+
+template <int DT, int RF, bool WIDE>
+__global__ void __launch_bounds__(kFewWaves * 64) few_kernel(const FewArgs f)
+{
+    constexpr int RP = RF * 16, PER = RP / 8, LD = 64 + 8, LDW = RP + 8, LDO = 64 + 4, LDV = 2 * RP + 8;
+    constexpr int STAGE = (64 * LDW > 32 * LD ? 64 * LDW : 32 * LD) * 2 > 16 * LDO * 4 ? (64 * LDW > 32 * LD ? 64 * LDW : 32 * LD) * 2 : 16 * LDO * 4;
+    static_assert(RF <= 2 && kFewWaves * STAGE >= kFewWaves * RF * 64 * 16);
+    __shared__ __attribute__((aligned(16))) unsigned char lds[kFewWaves * STAGE];
+    __shared__ __attribute__((aligned(16))) float sums[16 * (RP + 4)];
+    __shared__ __attribute__((aligned(16))) uint16_t sv[16 * LDV];
+    __shared__ float factor[16];
+    const AdapterArgs &a = f.p;
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int runs = (f.chunks + f.per - 1) / f.per, tile = blockIdx.x / runs, run = blockIdx.x - tile * runs;
+    const int c0 = run * f.per, c1 = min(f.chunks, c0 + f.per);
+    // tokens without an adapter, 16 looked at by each tile, one a wave
+    if (a.y != a.add && (int64_t)tile * 16 + wave < a.T) {
+        const int64_t t = (int64_t)tile * 16 + wave;
+        if ((unsigned)a.slots[t] >= (unsigned)a.T)
+            for (int n = c0 * kFewCols + lane * 8; n < min(c1 * kFewCols, a.N); n += 512) {
+                Raw<DT> v = {};
+                if (a.add)
+                    v = load_piece<DT, WIDE>(a.add, t * a.N + n, a.N - n);
+                store_piece<DT, WIDE>(a.y, t * a.N + n, a.N - n, v);
+            }
+    }
+    int e, r0, r1;
+    if (!find_tile<16>(a.offsets, a.E, a.T, tile, e, r0, r1))
+        return;
+    int tok[2];  // of rows lane / 8 and 8 on
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+        tok[m] = token_at(a.order, r0 + m * 8 + lane / 8, r1, a.T);
+    const uint16_t *w = a.a + (int64_t)e * a.rank * a.K, *wb = a.b + (int64_t)e * a.rank * a.N;
+    unsigned char *mine = lds + wave * STAGE;
+    uint16_t *stage = reinterpret_cast<uint16_t *>(mine);
+    float *so = reinterpret_cast<float *>(mine);
+    auto order = []() { asm volatile("" ::: "memory"); };  // (a wave's LDS accesses are in order)
+    u32x4_v raw[PER];
+    Raw<DT> base[2];
+    auto fetch_up = [&](int c) {
+        const int n0 = c * kFewCols + wave * 64, n = n0 + lane % 8 * 8;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = (i * 64 + lane) / PER, j = (i * 64 + lane) % PER * 8;
+            raw[i] = n0 + r < a.N ? row_piece<WIDE>(wb + (int64_t)(n0 + r) * a.rank, j, a.rank) : u32x4_v{};
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            base[h] = Raw<DT>{};
+            if (a.add && tok[h] >= 0)
+                base[h] = load_piece<DT, WIDE>(a.add, (int64_t)tok[h] * a.N + n, a.N - n);
+        }
+    };
+    constexpr int B = RF == 1 ? 4 : 2;  // steps whose loads go out together
+    const int steps = (a.K + 63) / 64;
+    f32x4_t acc[RF] = {};
+    fetch_up(c0);
+    for (int i0 = wave; i0 < steps; i0 += B * kFewWaves) {
+        u32x4_v nx[B][2], nw[B][2 * RF];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int i = i0 + b * kFewWaves, k = i * 64 + lane % 8 * 8;  // (past the last step: past the rows' end)
+#pragma unroll
+            for (int q = 0; q < 2 * RF; ++q) {
+                const int j = q * 8 + lane / 8;
+                nw[b][q] = j < a.rank ? row_piece<WIDE>(w + (int64_t)j * a.K, k, a.K) : u32x4_v{};
+            }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                nx[b][m] = tok[m] >= 0 ? row_piece<WIDE>(a.x + (int64_t)tok[m] * a.K, k, a.K) : u32x4_v{};
+        }
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            if (i0 + b * kFewWaves >= steps)
+                break;
+            u32x4_v xf[2], wf[2][RF];
+            order();
+#pragma unroll
+            for (int q = 0; q < 2 * RF; ++q)
+                *reinterpret_cast<u32x4_v *>(stage + (q * 8 + lane / 8) * LD + lane % 8 * 8) = nw[b][q];
+            order();
+#pragma unroll
+            for (int u = 0; u < RF; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    wf[h][u] = *reinterpret_cast<const u32x4_v *>(stage + (u * 16 + col) * LD + h * 32 + g * 8);
+            order();
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+                *reinterpret_cast<u32x4_v *>(stage + (m * 8 + lane / 8) * LD + lane % 8 * 8) = nx[b][m];
+            order();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                xf[h] = *reinterpret_cast<const u32x4_v *>(stage + col * LD + h * 32 + g * 8);
+            order();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int u = 0; u < RF; ++u)
+                    acc[u] = mfma<DT>(wf[h][u], xf[h], acc[u]);
+        }
+    }
+    // the waves' sums
+    f32x4_t *parts = reinterpret_cast<f32x4_t *>(lds);
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < RF; ++u)
+        parts[(wave * RF + u) * 64 + lane] = acc[u];
+    __syncthreads();
+    if (wave < RF) {
+        f32x4_t v = parts[wave * 64 + lane];
+#pragma unroll
+        for (int u = 1; u < kFewWaves; ++u)
+            v += parts[(u * RF + wave) * 64 + lane];
+        *reinterpret_cast<f32x4_t *>(sums + col * (RP + 4) + wave * 16 + g * 4) = v;
+    }
+    __syncthreads();
+    if (tid < 16 * PER) {
+        const int row = tid / PER, j0 = tid % PER * 8, t = token_at(a.order, r0 + row, r1, a.T);
+        float v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            v[k] = sums[row * (RP + 4) + j0 + k];
+        if (a.hidden && run == 0 && t >= 0)
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (j0 + k < a.rank)
+                    a.hidden[(int64_t)t * a.rank + j0 + k] = v[k];
+        int ex = 0;
+        if constexpr (DT == TERNARY_FP16) {
+            float m = largest(v);
+#pragma unroll
+            for (int o = 1; o < PER; o <<= 1)
+                m = fmaxf(m, __shfl_xor(m, o));
+            ex = exponent(m);
+        }
+        put_split<DT, RP>(sv + row * LDV, j0, v, ex);
+        if (j0 == 0)
+            factor[row] = ldexpf(a.scale ? a.scale[e] : 1.f, ex);
+    }
+    __syncthreads();
+    for (int c = c0; c < c1; ++c) {
+        const int n = c * kFewCols + wave * 64 + lane % 8 * 8;
+        u32x4_v wf[4];
+        order();
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            *reinterpret_cast<u32x4_v *>(stage + (i * 64 + lane) / PER * LDW + (i * 64 + lane) % PER * 8) = raw[i];
+        order();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            wf[u] = *reinterpret_cast<const u32x4_v *>(stage + (u * 16 + col) * LDW + (RP < 32 ? (g & 1) * 8 : g * 8));
+        f32x4_t out[4] = {};
+#pragma unroll
+        for (int q = 0; q < RF; ++q) {
+            const u32x4_v vf = *reinterpret_cast<const u32x4_v *>(sv + col * LDV + q * 32 + g * 8);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                out[u] = mfma<DT>(wf[u], vf, out[u]);
+        }
+        const float by = factor[col];
+        order();
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            *reinterpret_cast<f32x4_t *>(so + col * LDO + u * 16 + g * 4) = out[u] * by;
+        order();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int row = h * 8 + lane / 8;
+            const f32x4_t lo = *reinterpret_cast<const f32x4_t *>(so + row * LDO + lane % 8 * 8);
+            const f32x4_t hi = *reinterpret_cast<const f32x4_t *>(so + row * LDO + lane % 8 * 8 + 4);
+            float o[8];
+            widen_piece(base[h], o);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] += i < 4 ? lo[i % 4] : hi[i % 4];
+            if (tok[h] >= 0 && n < a.N)
+                store_piece<DT, WIDE>(a.y, (int64_t)tok[h] * a.N + n, a.N - n, round_piece<DT>(o));
+        }
+        if (c + 1 < c1)
+            fetch_up(c + 1);
+    }
+}
+
 // ---------------------------------------------------------------- launches
 
 inline int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m; }
@@ -804,12 +1000,36 @@ hipError_t launch_up(UpArgs u, bool fp16, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Whether one launch takes all.  Us in a graph, one launch and two (from Python, where a launch and a workspace cost the
+// host 5: 10.1 and 15.1 wherever the kernels take less), 4096 -> N, 32 adapters.  Rank 16: 1 token -> 4096 7.3 and 7.8, 16 7.5 and
+// 7.8, 64 9.1 and 8.5, 128 -> 1024 8.4 and 8.4, 128 -> 4096 10.1 and 8.9, 64 -> 18944 15.2 and 12.2.  Rank 32: 1 -> 4096 9.0 and 8.5,
+// 4 9.2 and 8.6, 16 10.6 and 8.8, 64 11.8 and 10.5.
+inline bool few_tokens(int64_t T, int64_t N, int64_t rank)
+{
+    return rank <= 16 ? T <= 128 && T * N <= 1 << 18 : rank <= 32 && T * N <= 1 << 14;
+}
+
+hipError_t launch_few(const AdapterArgs &a, hipStream_t stream)
+{
+    FewArgs f = {a, (int)up_to(a.N, kFewCols), 1};
+    const int64_t tiles = tiles_of(a.T, a.E, 16);
+    f.per = (int)(tiles * f.chunks >= 512 ? (tiles * f.chunks >= 1024 ? 4 : 2) : 1);
+    const bool wide = a.K % 8 == 0 && a.N % 8 == 0 && a.rank % 8 == 0 && aligned16(a.x) && aligned16(a.a) && aligned16(a.b) &&
+                      aligned16(a.add) && aligned16(a.y);
+    const dim3 grid((unsigned)(tiles * up_to(f.chunks, f.per)));
+    with_rank(a.fp16, a.rank, wide, [&](auto dt, auto rf, auto wd) {
+        if constexpr (decltype(rf)::value <= 2)
+            hipLaunchKernelGGL((few_kernel<decltype(dt)::value, decltype(rf)::value, decltype(wd)::value>), grid,
+                               dim3(kFewWaves * 64), 0, stream, f);
+    });
+    return hipGetLastError();
+}
+
 }  // namespace
 
 int64_t adapters_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E)
 {
-    (void)N;
-    return small_bytes(T, E, K, rank);
+    return few_tokens(T, N, rank) ? 0 : small_bytes(T, E, K, rank);
 }
 
 int64_t adapters_back_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E)
@@ -820,6 +1040,8 @@ int64_t adapters_back_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, i
 
 hipError_t launch_adapters(const AdapterArgs &a, hipStream_t stream)
 {
+    if (few_tokens(a.T, a.N, a.rank))
+        return launch_few(a, stream);
     const int splits = down_splits(a.T, a.E, a.K, a.rank);
     float *v = static_cast<float *>(a.workspace);
     const DownArgs d = {a.x, a.a, nullptr, a.offsets, a.order, v, a.T, a.K, a.rank, a.E, splits};

@@ -186,13 +186,14 @@ int ternary_linear_adapters(const void *x, int dtype, int64_t T, int64_t K, int6
         return st;
     if (T == 0)
         return TERNARY_OK;
-    if (!x || !a || !b || !offsets || !order || !slots || !y || !workspace)
+    const int64_t wsbytes = ternary::adapters_workspace(T, K, N, rank, E);
+    if (!x || !a || !b || !offsets || !order || !slots || !y || (wsbytes && !workspace))
         return TERNARY_ERR_NULL;
     if (!aligned(x, 2) || !aligned(a, 2) || !aligned(b, 2) || !aligned(add, 2) || !aligned(y, 2) || !aligned(scale, 4) ||
         !aligned(offsets, 4) || !aligned(order, 4) || !aligned(slots, 4) || !aligned(hidden, 16) ||
-        !aligned(workspace, 16))
+        (wsbytes && !aligned(workspace, 16)))
         return TERNARY_ERR_ALIGN;
-    if (aliased({{y, 2 * T * N}, {hidden, 4 * T * rank}, {workspace, ternary::adapters_workspace(T, K, N, rank, E)}},
+    if (aliased({{y, 2 * T * N}, {hidden, 4 * T * rank}, {workspace, wsbytes}},
                 {{x, 2 * T * K}, {a, 2 * E * rank * K}, {b, 2 * E * N * rank}, {scale, 4 * E}, {offsets, 4 * (E + 1)},
                  {order, 4 * T}, {slots, 4 * T}},
                 {add, 2 * T * N}))

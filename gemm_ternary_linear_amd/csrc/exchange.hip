@@ -39,7 +39,7 @@ __device__ __forceinline__ float wave_add(float v)
     return v;
 }
 
-template <int DT, bool WIDE>
+template <int DT, bool WIDE, bool STREAM>
 __global__ void __launch_bounds__(kThreads) dispatch_kernel(const ExchangeArgs a)
 {
     const int64_t per = (a.N + 7) / 8, units = a.T * per, stride = (int64_t)gridDim.x * kThreads;
@@ -62,12 +62,12 @@ __global__ void __launch_bounds__(kThreads) dispatch_kernel(const ExchangeArgs a
                     s[i] = w * v[i];
                 y = round_piece<DT>(s);
             }
-            store_piece<DT, WIDE>(a.out, (int64_t)p * a.N + n, left, y);
+            store_piece<DT, WIDE, STREAM>(a.out, (int64_t)p * a.N + n, left, y);
         }
     }
 }
 
-template <int DT, bool WIDE>
+template <int DT, bool WIDE, bool STREAM>
 __global__ void __launch_bounds__(kThreads) combine_back_kernel(const ExchangeArgs a)
 {
     const int lane = threadIdx.x & 63;
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) combine_back_kernel(const ExchangeAr
                 const int n = n0 + b * 512;
                 if (n < a.N) {
                     g[b] = load_piece<DT, WIDE>(a.grad, t * a.N + n, a.N - n);
-                    y[b] = load_piece<DT, WIDE>(a.x, (int64_t)p * a.N + n, a.N - n);
+                    y[b] = load_piece<DT, WIDE, STREAM>(a.x, (int64_t)p * a.N + n, a.N - n);
                 }
             }
 #pragma unroll
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) combine_back_kernel(const ExchangeAr
                         sum += gv[i] * yv[i];
                         gv[i] *= w;
                     }
-                    store_piece<DT, WIDE>(a.out, (int64_t)p * a.N + n, a.N - n, round_piece<DT>(gv));
+                    store_piece<DT, WIDE, STREAM>(a.out, (int64_t)p * a.N + n, a.N - n, round_piece<DT>(gv));
                 }
             }
         }
@@ -196,15 +196,20 @@ bool wide_rows(const ExchangeArgs &a)
     return a.N % 8 == 0 && (((uintptr_t)a.x | (uintptr_t)a.grad | (uintptr_t)a.add | (uintptr_t)a.out) & 15) == 0;
 }
 
-// Runs f(dtype, wide rows) as compile-time values.
+// Runs f(dtype, wide rows, rows past the caches) as compile-time values.  16-bit rows of 64 MB or more go past the caches
+// (us, past and not: dispatch 2047 x 4096 27.2 and 30.8, combine's gradient 56 and 61; of 34 MB 8.1 and 9.7, 15.5 and 13.3; fp32 dispatch of 65 MB
+// 26.7 and 22.3).
 template <class F>
 void with_rows(const ExchangeArgs &a, int dtype, F f)
 {
+    const bool stream = dtype != TERNARY_FP32 && a.R * a.N >= (int64_t)32 << 20;
     with_dtype(dtype, [&](auto dt) {
-        if (wide_rows(a))
-            f(dt, std::true_type());
+        if (!wide_rows(a))
+            f(dt, std::false_type(), std::false_type());
+        else if (!stream)
+            f(dt, std::true_type(), std::false_type());
         else
-            f(dt, std::false_type());
+            f(dt, std::true_type(), std::true_type());
     });
 }
 
@@ -216,8 +221,9 @@ hipError_t launch_dispatch(const ExchangeArgs &a, int dtype, hipStream_t stream)
     // few pieces: the stores of one are shared out over several threads
     const int ways = wgs >= 512 ? 1 : (int)(512 / wgs < a.k ? 512 / wgs : a.k);
     const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : (1 << 20)), ways);
-    with_rows(a, dtype, [&](auto dt, auto wide) {
-        hipLaunchKernelGGL((dispatch_kernel<decltype(dt)::value, decltype(wide)::value>), grid, dim3(kThreads), 0, stream, a);
+    with_rows(a, dtype, [&](auto dt, auto wide, auto past) {
+        hipLaunchKernelGGL((dispatch_kernel<decltype(dt)::value, decltype(wide)::value, decltype(past)::value>), grid,
+                           dim3(kThreads), 0, stream, a);
     });
     return hipGetLastError();
 }
@@ -225,16 +231,17 @@ hipError_t launch_dispatch(const ExchangeArgs &a, int dtype, hipStream_t stream)
 hipError_t launch_combine_back(const ExchangeArgs &a, int dtype, hipStream_t stream)
 {
     const dim3 grid((unsigned)((a.T * a.k + kThreads / 64 - 1) / (kThreads / 64)));
-    with_rows(a, dtype, [&](auto dt, auto wide) {
-        hipLaunchKernelGGL((combine_back_kernel<decltype(dt)::value, decltype(wide)::value>), grid, dim3(kThreads), 0, stream, a);
+    with_rows(a, dtype, [&](auto dt, auto wide, auto past) {
+        hipLaunchKernelGGL((combine_back_kernel<decltype(dt)::value, decltype(wide)::value, decltype(past)::value>), grid,
+                           dim3(kThreads), 0, stream, a);
     });
     return hipGetLastError();
 }
 
 hipError_t launch_dispatch_back(const ExchangeArgs &a, int dtype, hipStream_t stream)
 {
-    const int threads = a.N <= 512 ? 64 : a.N <= 1024 ? 128 : kThreads;
-    with_rows(a, dtype, [&](auto dt, auto wide) {
+    const int threads = a.N <= 1024 ? 64 : a.N <= 2048 ? 128 : kThreads;  // two pieces a thread
+    with_rows(a, dtype, [&](auto dt, auto wide, auto) {
         constexpr int DT = decltype(dt)::value;
         constexpr bool WIDE = decltype(wide)::value;
         if (a.weights)

@@ -614,7 +614,8 @@ int ternary_combine_backward(const void *grad, const void *y, int dtype, int64_t
  *   y          [T, N] output.  A token without an adapter gets add, or 0.
  *   hidden     fp32 [T, rank] output x[t] a_e^T for the gradient, 16-byte aligned, or NULL; rows of tokens without an
  *              adapter are left as they were.
- *   workspace  device memory of ternary_linear_adapters_workspace() bytes, 16-byte aligned, written before it is read.
+ *   workspace  device memory of ternary_linear_adapters_workspace() bytes, 16-byte aligned (NULL where that is 0), written
+ *              before it is read.
  * The other pointers aligned to their elements' size; no output may overlap an input (but add) or another.
  * Products are exact and their sums fp32, in an order that depends on the sizes alone; x a^T enters the second
  * product as two 16-bit numbers, within 2^-16 of it (bf16; fp16: 2^-22 of the row's largest); y is rounded once.
@@ -625,7 +626,7 @@ int ternary_linear_adapters(const void *x, int dtype, int64_t T, int64_t K, int6
                             const int32_t *order, const int32_t *slots, const void *add, void *y, float *hidden,
                             void *workspace, hipStream_t stream);
 
-/* Bytes of its workspace, or TERNARY_ERR_SHAPE. */
+/* Bytes of its workspace (0 for few tokens of small rank), or TERNARY_ERR_SHAPE. */
 int64_t ternary_linear_adapters_workspace(int64_t T, int64_t K, int64_t N, int64_t rank, int64_t E);
 
 /*

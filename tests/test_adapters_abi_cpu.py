@@ -81,7 +81,7 @@ def test_combine_backward_refuses(tl, kw, status):
     assert combine_back(tl, **kw) == status
 
 
-def adapters(tl, x=F, dtype=0, T=8, K=256, N=128, rank=16, a=2 * F, b=3 * F, E=4, s=4 * F, off=5 * F, order=6 * F, slots=7 * F, add=None, y=8 * F,
+def adapters(tl, x=F, dtype=0, T=8, K=256, N=128, rank=64, a=2 * F, b=3 * F, E=4, s=4 * F, off=5 * F, order=6 * F, slots=7 * F, add=None, y=8 * F,
              hidden=9 * F, ws=10 * F):
     return tl.lib().ternary_linear_adapters(x, dtype, T, K, N, rank, a, b, E, s, off, order, slots, add, y, hidden, ws, None)
 
@@ -120,7 +120,8 @@ def test_adapters_backward_refuses(tl, kw, status):
 
 def test_adapters_workspaces(tl):
     f, g = tl.lib().ternary_linear_adapters_workspace, tl.lib().ternary_linear_adapters_backward_workspace
-    assert f(8, 256, 128, 16, 4) >= 4 * 8 * 16 and g(8, 256, 128, 16, 4) >= 4 * 8 * 16
+    assert f(8, 256, 128, 16, 4) == 0 and f(8, 256, 128, 64, 4) >= 4 * 8 * 64 and f(5000, 256, 128, 16, 4) >= 4 * 5000 * 16
+    assert g(8, 256, 128, 16, 4) >= 4 * 8 * 16
     assert f(0, 256, 128, 16, 4) >= 0 and g(0, 256, 128, 16, 4) >= 0
     assert f(8, 0, 128, 16, 4) == g(8, 256, 128, 129, 4) == SHAPE
     assert f(1 << 20, 4096, 4096, 128, 512) > 0 and g(1 << 20, 4096, 4096, 128, 512) > 0
