@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kThreads) outer_sum_kernel(const OuterArgs a, 
 // L2), which costs less than a second launch; b and what is added to are under way meanwhile.
 struct FewArgs {
     AdapterArgs p;
-    int chunks, per;  // runs of 1024 columns; how many a workgroup takes
+    int chunks;  // runs of 1024 columns
 };
 constexpr int kFewWaves = 16, kFewCols = kFewWaves * 64;
 
@@ -722,13 +722,12 @@ __global__ void __launch_bounds__(kFewWaves * 64) few_kernel(const FewArgs f)
     const AdapterArgs &a = f.p;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, col = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int runs = (f.chunks + f.per - 1) / f.per, tile = blockIdx.x / runs, run = blockIdx.x - tile * runs;
-    const int c0 = run * f.per, c1 = min(f.chunks, c0 + f.per);
+    const int tile = blockIdx.x / f.chunks, chunk = blockIdx.x - tile * f.chunks;
     // tokens without an adapter, 16 looked at by each tile, one a wave
     if (a.y != a.add && (int64_t)tile * 16 + wave < a.T) {
         const int64_t t = (int64_t)tile * 16 + wave;
         if ((unsigned)a.slots[t] >= (unsigned)a.T)
-            for (int n = c0 * kFewCols + lane * 8; n < min(c1 * kFewCols, a.N); n += 512) {
+            for (int n = chunk * kFewCols + lane * 8; n < min((chunk + 1) * kFewCols, a.N); n += 512) {
                 Raw<DT> v = {};
                 if (a.add)
                     v = load_piece<DT, WIDE>(a.add, t * a.N + n, a.N - n);
@@ -747,26 +746,23 @@ __global__ void __launch_bounds__(kFewWaves * 64) few_kernel(const FewArgs f)
     uint16_t *stage = reinterpret_cast<uint16_t *>(mine);
     float *so = reinterpret_cast<float *>(mine);
     auto order = []() { asm volatile("" ::: "memory"); };  // (a wave's LDS accesses are in order)
+    const int n0 = chunk * kFewCols + wave * 64, n = n0 + lane % 8 * 8;  // this wave's columns, this lane's
     u32x4_v raw[PER];
     Raw<DT> base[2];
-    auto fetch_up = [&](int c) {
-        const int n0 = c * kFewCols + wave * 64, n = n0 + lane % 8 * 8;
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = (i * 64 + lane) / PER, j = (i * 64 + lane) % PER * 8;
-            raw[i] = n0 + r < a.N ? row_piece<WIDE>(wb + (int64_t)(n0 + r) * a.rank, j, a.rank) : u32x4_v{};
-        }
+    for (int i = 0; i < PER; ++i) {
+        const int r = (i * 64 + lane) / PER, j = (i * 64 + lane) % PER * 8;
+        raw[i] = n0 + r < a.N ? row_piece<WIDE>(wb + (int64_t)(n0 + r) * a.rank, j, a.rank) : u32x4_v{};
+    }
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            base[h] = Raw<DT>{};
-            if (a.add && tok[h] >= 0)
-                base[h] = load_piece<DT, WIDE>(a.add, (int64_t)tok[h] * a.N + n, a.N - n);
-        }
-    };
+    for (int h = 0; h < 2; ++h) {
+        base[h] = Raw<DT>{};
+        if (a.add && tok[h] >= 0)
+            base[h] = load_piece<DT, WIDE>(a.add, (int64_t)tok[h] * a.N + n, a.N - n);
+    }
     constexpr int B = RF == 1 ? 4 : 2;  // steps whose loads go out together
     const int steps = (a.K + 63) / 64;
     f32x4_t acc[RF] = {};
-    fetch_up(c0);
     for (int i0 = wave; i0 < steps; i0 += B * kFewWaves) {
         u32x4_v nx[B][2], nw[B][2 * RF];
 #pragma unroll
@@ -833,7 +829,7 @@ __global__ void __launch_bounds__(kFewWaves * 64) few_kernel(const FewArgs f)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             v[k] = sums[row * (RP + 4) + j0 + k];
-        if (a.hidden && run == 0 && t >= 0)
+        if (a.hidden && chunk == 0 && t >= 0)
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 if (j0 + k < a.rank)
@@ -851,46 +847,41 @@ __global__ void __launch_bounds__(kFewWaves * 64) few_kernel(const FewArgs f)
             factor[row] = ldexpf(a.scale ? a.scale[e] : 1.f, ex);
     }
     __syncthreads();
-    for (int c = c0; c < c1; ++c) {
-        const int n = c * kFewCols + wave * 64 + lane % 8 * 8;
-        u32x4_v wf[4];
-        order();
+    u32x4_v wf[4];
+    order();
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            *reinterpret_cast<u32x4_v *>(stage + (i * 64 + lane) / PER * LDW + (i * 64 + lane) % PER * 8) = raw[i];
-        order();
+    for (int i = 0; i < PER; ++i)
+        *reinterpret_cast<u32x4_v *>(stage + (i * 64 + lane) / PER * LDW + (i * 64 + lane) % PER * 8) = raw[i];
+    order();
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-            wf[u] = *reinterpret_cast<const u32x4_v *>(stage + (u * 16 + col) * LDW + (RP < 32 ? (g & 1) * 8 : g * 8));
-        f32x4_t out[4] = {};
+    for (int u = 0; u < 4; ++u)
+        wf[u] = *reinterpret_cast<const u32x4_v *>(stage + (u * 16 + col) * LDW + (RP < 32 ? (g & 1) * 8 : g * 8));
+    f32x4_t out[4] = {};
 #pragma unroll
-        for (int q = 0; q < RF; ++q) {
-            const u32x4_v vf = *reinterpret_cast<const u32x4_v *>(sv + col * LDV + q * 32 + g * 8);
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                out[u] = mfma<DT>(wf[u], vf, out[u]);
-        }
-        const float by = factor[col];
-        order();
+    for (int q = 0; q < RF; ++q) {
+        const u32x4_v vf = *reinterpret_cast<const u32x4_v *>(sv + col * LDV + q * 32 + g * 8);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
-            *reinterpret_cast<f32x4_t *>(so + col * LDO + u * 16 + g * 4) = out[u] * by;
-        order();
+            out[u] = mfma<DT>(wf[u], vf, out[u]);
+    }
+    const float by = factor[col];
+    order();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int row = h * 8 + lane / 8;
-            const f32x4_t lo = *reinterpret_cast<const f32x4_t *>(so + row * LDO + lane % 8 * 8);
-            const f32x4_t hi = *reinterpret_cast<const f32x4_t *>(so + row * LDO + lane % 8 * 8 + 4);
-            float o[8];
-            widen_piece(base[h], o);
+    for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<f32x4_t *>(so + col * LDO + u * 16 + g * 4) = out[u] * by;
+    order();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                o[i] += i < 4 ? lo[i % 4] : hi[i % 4];
-            if (tok[h] >= 0 && n < a.N)
-                store_piece<DT, WIDE>(a.y, (int64_t)tok[h] * a.N + n, a.N - n, round_piece<DT>(o));
-        }
-        if (c + 1 < c1)
-            fetch_up(c + 1);
+    for (int h = 0; h < 2; ++h) {
+        const int row = h * 8 + lane / 8;
+        const f32x4_t lo = *reinterpret_cast<const f32x4_t *>(so + row * LDO + lane % 8 * 8);
+        const f32x4_t hi = *reinterpret_cast<const f32x4_t *>(so + row * LDO + lane % 8 * 8 + 4);
+        float o[8];
+        widen_piece(base[h], o);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] += i < 4 ? lo[i % 4] : hi[i % 4];
+        if (tok[h] >= 0 && n < a.N)
+            store_piece<DT, WIDE>(a.y, (int64_t)tok[h] * a.N + n, a.N - n, round_piece<DT>(o));
     }
 }
 
@@ -1011,12 +1002,10 @@ inline bool few_tokens(int64_t T, int64_t N, int64_t rank)
 
 hipError_t launch_few(const AdapterArgs &a, hipStream_t stream)
 {
-    FewArgs f = {a, (int)up_to(a.N, kFewCols), 1};
-    const int64_t tiles = tiles_of(a.T, a.E, 16);
-    f.per = (int)(tiles * f.chunks >= 512 ? (tiles * f.chunks >= 1024 ? 4 : 2) : 1);
+    const FewArgs f = {a, (int)up_to(a.N, kFewCols)};
     const bool wide = a.K % 8 == 0 && a.N % 8 == 0 && a.rank % 8 == 0 && aligned16(a.x) && aligned16(a.a) && aligned16(a.b) &&
                       aligned16(a.add) && aligned16(a.y);
-    const dim3 grid((unsigned)(tiles * up_to(f.chunks, f.per)));
+    const dim3 grid((unsigned)(tiles_of(a.T, a.E, 16) * f.chunks));
     with_rank(a.fp16, a.rank, wide, [&](auto dt, auto rf, auto wd) {
         if constexpr (decltype(rf)::value <= 2)
             hipLaunchKernelGGL((few_kernel<decltype(dt)::value, decltype(rf)::value, decltype(wd)::value>), grid,
