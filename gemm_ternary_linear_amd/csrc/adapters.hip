@@ -201,6 +201,9 @@ struct DownArgs {
 // cache lines), the next turn's loads under way meanwhile, and meet at the end.  Rows are loaded as they lie, eight
 // neighbouring lanes a line, and pass through LDS into operands: loaded as operands, with neighbouring lanes
 // in different rows, each lane would cost L1 an access.
+//
+// HBM-bound at small ranks; at larger ones the weights, read from L2 for every tile, weigh as much.  Measured (8191 tokens of 4096,
+// in a graph; a copy's rate 13.5 us): rank 16 13.6, 32 15.0, 64 18.9 (25.3 before rows passed through LDS), 128 36.
 template <int DT, int RF, int MF, int WAVES, bool TR, bool WIDE>
 __global__ void __launch_bounds__(WAVES * 64) down_kernel(const DownArgs a)
 {
@@ -337,6 +340,10 @@ struct UpArgs {
 // A workgroup takes 16 MF places and runs of 256 columns, 64 a wave, whose weights stay in registers while the places
 // pass.  Weights, what is added to and y go between memory and the wave as they lie, eight neighbouring lanes a line, and
 // pass through LDS into operands and out of results, a wave by itself.
+//
+// HBM-bound.  Measured (8191 tokens, base and result, in a graph): 18944 columns 114 us at rank 16 (5.4 TB/s), 135 at rank 64, 179 at 128; 4096
+// columns at rank 32 29.4 (4.6 TB/s).  In the operands' own layout, 64 L1 accesses an instruction, it took 164 at rank 64; without
+// passing the caches 151.
 template <int DT, int RF, int MF, bool TR, bool WIDE>
 __global__ void __launch_bounds__(kThreads) up_kernel(const UpArgs a)
 {
@@ -507,6 +514,9 @@ struct OuterArgs {
 // A workgroup takes a piece of an adapter's tokens and 256 columns (128 of ranks 33 to 64): 64 a wave (32 of ranks above
 // 32), every second 32 tokens to each half of the waves, whose sums meet at the end.  Steps of 64 tokens pass through LDS as they lie, and both operands are
 // read transposed; the next step's loads are under way meanwhile.
+//
+// Bound by the latency of a step's loads (1.6 waves a SIMD): 8191 tokens of 4096 + 4096 columns at rank 32 35 us for 134 MB (3.8 TB/s), rank 64
+// 60; 512 tokens 8.
 // BY_RANK: the output is [E, rank, C], else [E, C, rank].
 template <int DT, int RF, bool WIDE, bool BY_RANK>
 __device__ __forceinline__ void outer_piece(const OuterArgs &a, const OuterProblem &p, int idx, int c0, uint16_t *sd,
@@ -702,7 +712,8 @@ __global__ void __launch_bounds__(kThreads) outer_sum_kernel(const OuterArgs a, 
 
 // Few tokens of small rank: down and up in one launch.  A workgroup of 16 waves takes 16 places: its waves share the rows of x,
 // meet, and take 64 columns of y each.  Workgroups that share the places each compute v for themselves (from
-// L2), which costs less than a second launch; b and what is added to are under way meanwhile.
+// L2), which costs less than a second launch; b and what is added to are under way meanwhile.  Bound by a chain of loads (offsets,
+// order, x and a, y): 1 token of 4096 x 4096, rank 16, 7.1 us in a graph, 64 tokens of 32 adapters 8.8.
 struct FewArgs {
     AdapterArgs p;
     int chunks;  // runs of 1024 columns
@@ -892,20 +903,24 @@ inline int64_t up_to(int64_t n, int64_t m) { return (n + m - 1) / m; }
 inline int64_t tiles_of(int64_t T, int64_t E, int64_t rows) { return T / rows + (E < T ? E : T); }
 inline bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
 
-// Fragments of 16 tokens of a down tile.  A workgroup has four waves; where tiles are few 16, so that there are few partial
-// sums (not of ranks above 32, which want the registers).
-inline int down_rows(int64_t T, int64_t E, int64_t rank) { return T <= 16 * E ? 1 : T >= 4096 && rank > 32 && rank <= 64 ? 4 : 2; }
-inline int64_t down_tiles(int64_t T, int64_t E, int64_t rank) { return up_to(T, 16 * down_rows(T, E, rank)) + (E < T ? E : T) / 2; }
-inline bool down_few(int64_t T, int64_t E, int64_t rank) { return rank <= 32 && down_tiles(T, E, rank) < 192; }
+// Fragments of 16 tokens of a down tile (us of all kernels for two and four: 8191 tokens of 4096 -> 18944 at rank 64 157 and 165, their gradients
+// of 4096 x 4096 118 and 131; for two and one 157 and 161, 118 and 123; one where adapters have fewer tokens).  A workgroup has four waves;
+// where tiles are few 16, so that there are few partial sums (1000 tokens at rank 16 13.3 us, with four 14.0; gradients of 2048 32.3 and 34.1; not
+// of ranks above 32, which want the registers).
+inline int down_rows(int64_t T, int64_t E) { return T <= 16 * E ? 1 : 2; }
+inline int64_t down_tiles(int64_t T, int64_t E) { return up_to(T, 16 * down_rows(T, E)) + (E < T ? E : T) / 2; }
+inline bool down_few(int64_t T, int64_t E, int64_t rank) { return rank <= 32 && down_tiles(T, E) < 192; }
 // Workgroups that share a row: until there are enough waves, or a wave has a single step.
 inline int down_splits(int64_t T, int64_t E, int64_t L, int64_t rank)
 {
-    const int64_t tiles = down_tiles(T, E, rank), waves = down_few(T, E, rank) ? 16 : 4, steps = up_to(L, 64 * waves);
+    const int64_t tiles = down_tiles(T, E), waves = down_few(T, E, rank) ? 16 : 4, steps = up_to(L, 64 * waves);
     int s = 1;
     while (s < 8 && s * 2 <= steps && s * tiles * waves < 1536)
         s *= 2;
     return s;
 }
+// Tokens of a piece: about 256 workgroups (of 8191 tokens, 4096 + 4096 columns; us of all gradients in a graph, for 192, 256 and 512: rank 32
+// 96, 97 and 104; rank 16 86, 86 and 93; 4096 tokens of 16 adapters, rank 128, 104, 103 and 117 for 384).
 inline int piece_tokens(int64_t T, int64_t K, int64_t N, int64_t rank)
 {
     const int cols = outer_cols(rank_frags(rank));
@@ -947,7 +962,7 @@ void with_rank(bool fp16, int rank, bool wide, F f)
 template <bool TR>
 hipError_t launch_down(const DownArgs &d, bool fp16, hipStream_t stream)
 {
-    const int mf = down_rows(d.T, d.E, d.rank);
+    const int mf = down_rows(d.T, d.E);
     const bool few = down_few(d.T, d.E, d.rank);
     const bool wide = d.L % 8 == 0 && aligned16(d.x) && aligned16(d.w) && (!TR || d.rank % 8 == 0);
     const dim3 grid((unsigned)(tiles_of(d.T, d.E, 16 * mf) * d.splits));
@@ -961,10 +976,6 @@ hipError_t launch_down(const DownArgs &d, bool fp16, hipStream_t stream)
             if (few)
                 return mf == 1 ? run(down_kernel<DT, RF, 1, 16, TR, WIDE>, 16) : run(down_kernel<DT, RF, 2, 16, TR, WIDE>, 16);
         }
-        if constexpr (RF == 4) {
-            if (mf == 4)
-                return run(down_kernel<DT, RF, 4, 4, TR, WIDE>, 4);
-        }
         mf == 1 ? run(down_kernel<DT, RF, 1, 4, TR, WIDE>, 4) : run(down_kernel<DT, RF, 2, 4, TR, WIDE>, 4);
     });
     return hipGetLastError();
@@ -974,7 +985,10 @@ template <bool TR>
 hipError_t launch_up(UpArgs u, bool fp16, hipStream_t stream)
 {
     u.chunks = (int)up_to(u.C, kCols);
-    const int mf = u.T <= 2048 ? 2 : 4;
+    // Large outputs: tiles of 64 places, past the caches (us, 64 and 32: 8191 tokens of 18944 columns at rank 64 165 and 197, 4096 of 8192
+    // at rank 128 87 and 89, 5000 of 4096 33.0 and 33.4 at rank 16, 51.6 and 50.3 at 64; 3000 of 4096 23.4 and 21.3, 32.1 and 27.5; 300 11.6 and
+    // 9.8).  Two runs of columns a workgroup where there are enough (18944 columns 135 us for up alone, one run 144).
+    const int mf = (int64_t)u.T * u.C >= (int64_t)3 << 23 ? 4 : 2;
     const int64_t tiles = tiles_of(u.T, u.E, 16 * mf);
     const int64_t per = tiles * u.chunks / 2048;
     u.per = (int)(per < 1 ? 1 : per > 2 ? 2 : per);

@@ -12,6 +12,9 @@
 // from caches at best).  combine's gradient takes a wave a slot: no sums across waves, and
 // as many waves as rows.  dispatch's gradient takes a workgroup a token, which holds its piece of x
 // and of dx in registers while the k rows pass.
+//
+// Measured (calls in a graph, bf16, 8 slots a token; a copy's rate in brackets): dispatch 2047 x 4096 27.4 us (30.3), combine's gradient 55.4
+// (57.3), dispatch's gradient 4096 x 2048 with weights and add 43.9 (37.2; one piece a thread 49).
 #include "fp8_common.h"
 #include "internal.h"
 #include "places.h"
@@ -218,7 +221,7 @@ void with_rows(const ExchangeArgs &a, int dtype, F f)
 hipError_t launch_dispatch(const ExchangeArgs &a, int dtype, hipStream_t stream)
 {
     const int64_t units = a.T * ((a.N + 7) / 8), wgs = (units + kThreads - 1) / kThreads;
-    // few pieces: the stores of one are shared out over several threads
+    // few pieces: the stores of one are shared out over several threads (8 rows each: 4 x 4096 3.1 us, one thread 4.7; 33 x 4096 3.1 and 4.9)
     const int ways = wgs >= 512 ? 1 : (int)(512 / wgs < a.k ? 512 / wgs : a.k);
     const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : (1 << 20)), ways);
     with_rows(a, dtype, [&](auto dt, auto wide, auto past) {

@@ -212,7 +212,8 @@ def test_adapters_backward(tl, T, E, rank, K, N, dtype):
 
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,E,rank,K,N", [(2049, 3, 16, 136, 264), (2500, 40, 32, 264, 520), (4200, 5, 64, 264, 520), (4200, 2, 40, 77, 139),
-                                          (5000, 1, 128, 264, 264), (9000, 7, 8, 1032, 72), (20000, 300, 16, 64, 320)])
+                                          (5000, 1, 128, 264, 264), (9000, 7, 8, 1032, 72), (20000, 300, 16, 64, 320), (7001, 2, 24, 3600, 4001),
+                                          (6500, 3, 48, 4000, 4096), (8200, 2, 90, 3201, 3104)])
 def test_adapters_many_tokens(tl, T, E, rank, K, N, dtype):
     """Whole numbers again, at numbers of tokens that take the kernels' large tiles and several pieces of an adapter's tokens
     (the definitions here on the GPU, in 64 bits)."""
@@ -237,7 +238,7 @@ def test_adapters_many_tokens(tl, T, E, rank, K, N, dtype):
         dx[at] += dv @ a[e]
         da[e], db[e] = dv.t().contiguous() @ x[at], gr[at].t().contiguous() @ hidden[at]
     for t in (v, y, dx, da, db):  # every sum fits 24 bits: |dv| and |v| below 2^16, and what they are multiplied and added up to
-        assert float(t.abs().max()) < 2.0 ** 22
+        assert float(t.abs().max()) < 2.0 ** 23
     r = tl.sort_slots(of.int(), E)
     hid = torch.zeros(T, rank, device="cuda")
     args = [t.to(dt) for t in (x, a, b)]

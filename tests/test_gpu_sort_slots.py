@@ -30,7 +30,7 @@ def check(tl, ids, E, what):
 
 @pytest.mark.parametrize("T,k,E", [(0, 2, 8), (1, 1, 1), (1, 32, 512), (2, 3, 3), (63, 1, 5), (64, 1, 32), (65, 1, 512), (100, 7, 40), (128, 8, 64),
                                    (129, 8, 64), (512, 8, 200), (513, 8, 200), (4096, 1, 33), (4097, 1, 33), (5000, 2, 512), (8192, 8, 256),
-                                   (8193, 8, 256), (12000, 8, 300), (16384, 8, 77), (16385, 8, 64), (131073, 1, 17), (70000, 4, 511)])
+                                   (8193, 8, 256), (12000, 8, 300), (16384, 8, 77), (16385, 8, 64), (131073, 1, 17), (262144, 1, 90), (70000, 4, 511)])
 def test_sort(tl, T, k, E):
     rng = np.random.default_rng(T + E)
     ids = rng.integers(0, E, (T, k)).astype(np.int32)
