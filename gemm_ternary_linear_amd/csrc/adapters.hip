@@ -203,7 +203,7 @@ struct DownArgs {
 // in different rows, each lane would cost L1 an access.
 //
 // HBM-bound at small ranks; at larger ones the weights, read from L2 for every tile, weigh as much.  Measured (8191 tokens of 4096,
-// in a graph; a copy's rate 13.5 us): rank 16 13.6, 32 15.0, 64 18.9 (25.3 before rows passed through LDS), 128 36.
+// in a graph; a copy's rate 13.5 us): rank 16 13.9, 32 15.0, 64 20.1 (in operands' layout 30.3), 128 41.
 template <int DT, int RF, int MF, int WAVES, bool TR, bool WIDE>
 __global__ void __launch_bounds__(WAVES * 64) down_kernel(const DownArgs a)
 {

@@ -17,6 +17,9 @@ namespace {
 // Most elements of a matrix: offsets are 64-bit, grids stay inside the launch limits.
 constexpr int64_t kMaxElems = (int64_t)1 << 38;
 
+// Most columns of all adapters: a launch holds a workgroup for each of them and run of columns.
+constexpr int64_t kMaxWidth = (int64_t)1 << 28;
+
 int64_t elem_bytes(int dtype)
 {
     return dtype == TERNARY_BF16 || dtype == TERNARY_FP16 ? 2 : dtype == TERNARY_FP32 ? 4 : 0;
@@ -66,7 +69,7 @@ int adapters_shape(int dtype, int64_t T, int64_t K, int64_t N, int64_t rank, int
     if (dtype != TERNARY_BF16 && dtype != TERNARY_FP16)
         return TERNARY_ERR_DTYPE;
     if (!dim_ok(T, 0) || !dim_ok(K, 1) || !dim_ok(N, 1) || !dim_ok(rank, 1, TERNARY_MAX_RANK) ||
-        !dim_ok(E, 1, TERNARY_MAX_EXPERTS) || T * K > kMaxElems || T * N > kMaxElems)
+        !dim_ok(E, 1, TERNARY_MAX_EXPERTS) || T * K > kMaxElems || T * N > kMaxElems || E * (K + N) > kMaxWidth)
         return TERNARY_ERR_SHAPE;
     return TERNARY_OK;
 }

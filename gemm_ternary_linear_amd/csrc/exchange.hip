@@ -25,6 +25,7 @@ namespace ternary {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int64_t kMostWgs = 1 << 20;  // workgroups of a launch; they take what is left in turns
 
 // The sum over a wave, in lane 63.
 __device__ __forceinline__ float wave_add(float v)
@@ -74,45 +75,46 @@ template <int DT, bool WIDE, bool STREAM>
 __global__ void __launch_bounds__(kThreads) combine_back_kernel(const ExchangeArgs a)
 {
     const int lane = threadIdx.x & 63;
-    const int64_t s = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (s >= a.T * a.k)
-        return;
-    const int64_t t = s / a.k;
-    const int p = a.slots[s];
-    float sum = 0.f;
-    if (p >= 0 && p < a.R) {
-        const float w = a.weights[s];
-        constexpr int B = DT == TERNARY_FP32 ? 2 : 4;  // pieces whose loads go out together
-        for (int n0 = lane * 8; n0 < a.N; n0 += B * 512) {
-            Raw<DT> g[B], y[B];
+    constexpr int W = kThreads / 64;
+    const int64_t first = (int64_t)blockIdx.x * W + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int64_t s = first; s < a.T * a.k; s += (int64_t)gridDim.x * W) {
+        const int64_t t = s / a.k;
+        const int p = a.slots[s];
+        float sum = 0.f;
+        if (p >= 0 && p < a.R) {
+            const float w = a.weights[s];
+            constexpr int B = DT == TERNARY_FP32 ? 2 : 4;  // pieces whose loads go out together
+            for (int n0 = lane * 8; n0 < a.N; n0 += B * 512) {
+                Raw<DT> g[B], y[B];
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int n = n0 + b * 512;
-                if (n < a.N) {
-                    g[b] = load_piece<DT, WIDE>(a.grad, t * a.N + n, a.N - n);
-                    y[b] = load_piece<DT, WIDE, STREAM>(a.x, (int64_t)p * a.N + n, a.N - n);
-                }
-            }
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int n = n0 + b * 512;
-                if (n < a.N) {
-                    float gv[8], yv[8];
-                    widen_piece(g[b], gv);
-                    widen_piece(y[b], yv);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        sum += gv[i] * yv[i];
-                        gv[i] *= w;
+                for (int b = 0; b < B; ++b) {
+                    const int n = n0 + b * 512;
+                    if (n < a.N) {
+                        g[b] = load_piece<DT, WIDE>(a.grad, t * a.N + n, a.N - n);
+                        y[b] = load_piece<DT, WIDE, STREAM>(a.x, (int64_t)p * a.N + n, a.N - n);
                     }
-                    store_piece<DT, WIDE, STREAM>(a.out, (int64_t)p * a.N + n, a.N - n, round_piece<DT>(gv));
+                }
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    const int n = n0 + b * 512;
+                    if (n < a.N) {
+                        float gv[8], yv[8];
+                        widen_piece(g[b], gv);
+                        widen_piece(y[b], yv);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            sum += gv[i] * yv[i];
+                            gv[i] *= w;
+                        }
+                        store_piece<DT, WIDE, STREAM>(a.out, (int64_t)p * a.N + n, a.N - n, round_piece<DT>(gv));
+                    }
                 }
             }
         }
+        sum = wave_add(sum);
+        if (lane == 63)
+            a.dweights[s] = sum;
     }
-    sum = wave_add(sum);
-    if (lane == 63)
-        a.dweights[s] = sum;
 }
 
 // WEIGHTED: rows times their weights, and the weights' gradient; else both left out.
@@ -122,75 +124,78 @@ __global__ void __launch_bounds__(kThreads) dispatch_back_kernel(const ExchangeA
     constexpr int C = 2, J = 4;  // pieces a thread holds at a time; rows whose loads go out together
     __shared__ float dots[kThreads / 64][TERNARY_MAX_TOP_K];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-    const int64_t t = blockIdx.x;
-    const int32_t *slots = a.slots + t * a.k;
-    if (WEIGHTED && lane < a.k)
-        dots[wave][lane] = 0.f;
-    for (int base = 0; base < a.N; base += C * 8 * blockDim.x) {
-        float acc[C][8], x[C][8];
-        int n[C], left[C];
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+        const int32_t *slots = a.slots + t * a.k;
+        if (WEIGHTED && lane < a.k)
+            dots[wave][lane] = 0.f;
+        for (int base = 0; base < a.N; base += C * 8 * blockDim.x) {
+            float acc[C][8], x[C][8];
+            int n[C], left[C];
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            n[c] = base + (c * blockDim.x + threadIdx.x) * 8;
-            left[c] = a.N - n[c];
+            for (int c = 0; c < C; ++c) {
+                n[c] = base + (c * blockDim.x + threadIdx.x) * 8;
+                left[c] = a.N - n[c];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                acc[c][i] = x[c][i] = 0.f;
-            if (left[c] > 0) {
-                if (a.add)
-                    widen_piece(load_piece<DT, WIDE>(a.add, t * a.N + n[c], left[c]), acc[c]);
-                if (WEIGHTED)
-                    widen_piece(load_piece<DT, WIDE>(a.x, t * a.N + n[c], left[c]), x[c]);
+                for (int i = 0; i < 8; ++i)
+                    acc[c][i] = x[c][i] = 0.f;
+                if (left[c] > 0) {
+                    if (a.add)
+                        widen_piece(load_piece<DT, WIDE>(a.add, t * a.N + n[c], left[c]), acc[c]);
+                    if (WEIGHTED)
+                        widen_piece(load_piece<DT, WIDE>(a.x, t * a.N + n[c], left[c]), x[c]);
+                }
             }
-        }
-        for (int j0 = 0; j0 < a.k; j0 += J) {
-            Raw<DT> g[J][C] = {};
-            float w[J];
+            for (int j0 = 0; j0 < a.k; j0 += J) {
+                Raw<DT> g[J][C] = {};
+                float w[J];
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const int p = j0 + j < a.k ? slots[j0 + j] : -1;
-                const bool has = p >= 0 && p < a.R;
-                w[j] = WEIGHTED ? (has ? a.weights[t * a.k + j0 + j] : 0.f) : 1.f;
-                if (has)
+                for (int j = 0; j < J; ++j) {
+                    const int p = j0 + j < a.k ? slots[j0 + j] : -1;
+                    const bool has = p >= 0 && p < a.R;
+                    w[j] = WEIGHTED ? (has ? a.weights[t * a.k + j0 + j] : 0.f) : 1.f;
+                    if (has)
 #pragma unroll
-                    for (int c = 0; c < C; ++c)
-                        if (left[c] > 0)
-                            g[j][c] = load_piece<DT, WIDE>(a.grad, (int64_t)p * a.N + n[c], left[c]);
-            }
+                        for (int c = 0; c < C; ++c)
+                            if (left[c] > 0)
+                                g[j][c] = load_piece<DT, WIDE>(a.grad, (int64_t)p * a.N + n[c], left[c]);
+                }
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                float dot = 0.f;
+                for (int j = 0; j < J; ++j) {
+                    float dot = 0.f;
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    float v[8];
-                    widen_piece(g[j][c], v);
+                    for (int c = 0; c < C; ++c) {
+                        float v[8];
+                        widen_piece(g[j][c], v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        acc[c][i] += WEIGHTED ? w[j] * v[i] : v[i];
-                        dot += WEIGHTED ? v[i] * x[c][i] : 0.f;
+                        for (int i = 0; i < 8; ++i) {
+                            acc[c][i] += WEIGHTED ? w[j] * v[i] : v[i];
+                            dot += WEIGHTED ? v[i] * x[c][i] : 0.f;
+                        }
+                    }
+                    if (WEIGHTED && j0 + j < a.k) {
+                        dot = wave_add(dot);
+                        if (lane == 63)
+                            dots[wave][j0 + j] += dot;
                     }
                 }
-                if (WEIGHTED && j0 + j < a.k) {
-                    dot = wave_add(dot);
-                    if (lane == 63)
-                        dots[wave][j0 + j] += dot;
-                }
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (left[c] > 0)
+                    store_piece<DT, WIDE>(a.out, t * a.N + n[c], left[c], round_piece<DT>(acc[c]));
+        }
+        if (WEIGHTED) {
+            __syncthreads();
+            if ((int)threadIdx.x < a.k) {
+                const int p = slots[threadIdx.x];
+                float sum = 0.f;
+                for (int i = 0; i < waves; ++i)
+                    sum += dots[i][threadIdx.x];
+                a.dweights[t * a.k + threadIdx.x] = p >= 0 && p < a.R ? sum : 0.f;
             }
         }
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (left[c] > 0)
-                store_piece<DT, WIDE>(a.out, t * a.N + n[c], left[c], round_piece<DT>(acc[c]));
-    }
-    if (WEIGHTED) {
-        __syncthreads();
-        if ((int)threadIdx.x < a.k) {
-            const int p = slots[threadIdx.x];
-            float sum = 0.f;
-            for (int i = 0; i < waves; ++i)
-                sum += dots[i][threadIdx.x];
-            a.dweights[t * a.k + threadIdx.x] = p >= 0 && p < a.R ? sum : 0.f;
-        }
+        if (WEIGHTED)
+            __syncthreads();  // (the sums are read before the next token's begin)
     }
 }
 
@@ -223,7 +228,7 @@ hipError_t launch_dispatch(const ExchangeArgs &a, int dtype, hipStream_t stream)
     const int64_t units = a.T * ((a.N + 7) / 8), wgs = (units + kThreads - 1) / kThreads;
     // few pieces: the stores of one are shared out over several threads (8 rows each: 4 x 4096 3.1 us, one thread 4.7; 33 x 4096 3.1 and 4.9)
     const int ways = wgs >= 512 ? 1 : (int)(512 / wgs < a.k ? 512 / wgs : a.k);
-    const dim3 grid((unsigned)(wgs < (1 << 20) ? wgs : (1 << 20)), ways);
+    const dim3 grid((unsigned)(wgs < kMostWgs ? wgs : kMostWgs), ways);
     with_rows(a, dtype, [&](auto dt, auto wide, auto past) {
         hipLaunchKernelGGL((dispatch_kernel<decltype(dt)::value, decltype(wide)::value, decltype(past)::value>), grid,
                            dim3(kThreads), 0, stream, a);
@@ -233,7 +238,8 @@ hipError_t launch_dispatch(const ExchangeArgs &a, int dtype, hipStream_t stream)
 
 hipError_t launch_combine_back(const ExchangeArgs &a, int dtype, hipStream_t stream)
 {
-    const dim3 grid((unsigned)((a.T * a.k + kThreads / 64 - 1) / (kThreads / 64)));
+    const int64_t wgs = (a.T * a.k + kThreads / 64 - 1) / (kThreads / 64);
+    const dim3 grid((unsigned)(wgs < kMostWgs ? wgs : kMostWgs));
     with_rows(a, dtype, [&](auto dt, auto wide, auto past) {
         hipLaunchKernelGGL((combine_back_kernel<decltype(dt)::value, decltype(wide)::value, decltype(past)::value>), grid,
                            dim3(kThreads), 0, stream, a);
@@ -243,14 +249,15 @@ hipError_t launch_combine_back(const ExchangeArgs &a, int dtype, hipStream_t str
 
 hipError_t launch_dispatch_back(const ExchangeArgs &a, int dtype, hipStream_t stream)
 {
+    const dim3 grid((unsigned)(a.T < kMostWgs ? a.T : kMostWgs));
     const int threads = a.N <= 1024 ? 64 : a.N <= 2048 ? 128 : kThreads;  // two pieces a thread
     with_rows(a, dtype, [&](auto dt, auto wide, auto) {
         constexpr int DT = decltype(dt)::value;
         constexpr bool WIDE = decltype(wide)::value;
         if (a.weights)
-            hipLaunchKernelGGL((dispatch_back_kernel<DT, WIDE, true>), dim3((unsigned)a.T), dim3(threads), 0, stream, a);
+            hipLaunchKernelGGL((dispatch_back_kernel<DT, WIDE, true>), grid, dim3(threads), 0, stream, a);
         else
-            hipLaunchKernelGGL((dispatch_back_kernel<DT, WIDE, false>), dim3((unsigned)a.T), dim3(threads), 0, stream, a);
+            hipLaunchKernelGGL((dispatch_back_kernel<DT, WIDE, false>), grid, dim3(threads), 0, stream, a);
     });
     return hipGetLastError();
 }

@@ -10,7 +10,7 @@
 // slots into the workspace; sums over the chunks before each are made by the placing
 // workgroups themselves where the chunks are few, else by a kernel in between.
 //
-// Measured (us in a graph): 64 x 1 of 32 keys 3.8, 8192 x 8 of 256 8.4, 32768 x 8 12.8, 100000 x 4 of 64 13.1; latency of one or two launches.  Limits: 4096
+// Measured (us in a graph): 64 x 1 of 32 keys 3.4, 8192 x 8 of 256 8.4, 32768 x 8 12.8, 100000 x 4 of 64 13.1; latency of one or two launches.  Limits: 4096
 // slots in one launch and in two, 64 keys 5.8 and 6.0, 256 keys 7.5 and 7.0; sums by the placing workgroups and by a
 // kernel, 64 chunks of 256 keys 8.5 and 10.1, 94 of 64 7.3 and 9.3, 128 of 256 9.4 and 11.0; chunks of 1024 and of 4096 slots, 65536 slots 8.5
 // and 13.3, 262144 12.8 and 14.3, 400000 13.3 and 13.1.

@@ -607,7 +607,7 @@ int ternary_combine_backward(const void *grad, const void *y, int dtype, int64_t
  *   x          [T, K], dtype `dtype` (TERNARY_BF16 or TERNARY_FP16), as are a, b, add and y.
  *   a, b       [E, rank, K] and [E, N, rank]; an adapter of a smaller rank is filled up with zeros.
  *   T, K, N    0 <= T <= 2^24, 1 <= K, N <= 2^24, T * K and T * N up to 2^38; T == 0 is a successful no-op.
- *   rank, E    1 <= rank <= TERNARY_MAX_RANK, 1 <= E <= TERNARY_MAX_EXPERTS.
+ *   rank, E    1 <= rank <= TERNARY_MAX_RANK, 1 <= E <= TERNARY_MAX_EXPERTS, E * (K + N) up to 2^28.
  *   scale      fp32 [E], or NULL for 1.
  *   offsets, order, slots  of ternary_sort_slots with top_k = 1.
  *   add        [T, N] (the projection's output), or NULL for none; may be y itself.

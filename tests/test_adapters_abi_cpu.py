@@ -87,7 +87,8 @@ def adapters(tl, x=F, dtype=0, T=8, K=256, N=128, rank=64, a=2 * F, b=3 * F, E=4
 
 
 SHAPES = [(dict(dtype=2), DTYPE), (dict(dtype=-1), DTYPE), (dict(T=-1), SHAPE), (dict(K=0), SHAPE), (dict(N=0), SHAPE), (dict(rank=0), SHAPE),
-          (dict(rank=129), SHAPE), (dict(E=0), SHAPE), (dict(E=513), SHAPE), (dict(K=(1 << 24) + 1), SHAPE), (dict(T=1 << 24, N=1 << 15), SHAPE)]
+          (dict(rank=129), SHAPE), (dict(E=0), SHAPE), (dict(E=513), SHAPE), (dict(K=(1 << 24) + 1), SHAPE), (dict(T=1 << 24, N=1 << 15), SHAPE),
+          (dict(E=512, N=1 << 19), SHAPE)]
 
 
 @pytest.mark.parametrize("kw,status", SHAPES + [

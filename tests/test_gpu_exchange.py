@@ -178,6 +178,28 @@ def test_exchange_far(tl):
     assert bool(((dx[t].double() - want).abs() <= 2.0 ** -7 * want.abs() + 1e-6).all())
 
 
+def test_exchange_many_tokens(tl):
+    """More tokens and slots than a launch has workgroups."""
+    say("exchange many tokens")
+    T, k, N = 1100000, 5, 8
+    r = tl.sort_slots(torch.randint(-1, 9, (T, k), dtype=torch.int32, device="cuda"), 9, torch.rand(T, k, device="cuda"))
+    x, g = torch.randn(T, N, device="cuda"), torch.randn(T, N, device="cuda")
+    y = tl.dispatch(x, r, out=torch.zeros(T * k, N, device="cuda"))
+    has, at = r.slots >= 0, r.slots.long().clamp_min(0)
+    assert torch.equal(y[at][has], x[:, None, :].expand(T, k, N)[has])
+    dy, dw = tl.combine_backward(g, y, r, out=torch.zeros_like(y))
+    want = torch.where(has, (x.double() * g.double()).sum(1, keepdim=True), 0.0)
+    mags = (x.double() * g.double()).abs().sum(1, keepdim=True)
+    assert bool(((dw.double() - want).abs() <= 16 * ar.STEP * mags).all())  # eight products, eight sums
+    assert torch.equal(dy[at][has], (r.weights[:, :, None] * g[:, None, :])[has])
+    dx, dw = tl.dispatch_backward(dy, r, x=x)
+    w2 = torch.where(has, r.weights.double(), 0.0)
+    want = (w2 * w2).sum(1, keepdim=True) * g.double()
+    assert bool(((dx.double() - want).abs() <= 16 * ar.STEP * want.abs() + 1e-30).all())  # k products (and dy's), k sums, of one sign
+    want, mags = w2 * (x.double() * g.double()).sum(1, keepdim=True), w2 * mags
+    assert bool(((dw.double() - want).abs() <= 18 * ar.STEP * mags).all())
+
+
 def test_exchange_other_stream(tl):
     """Calls on a stream of their own, and captured and replayed, give the eager results."""
     say("exchange streams")
